@@ -35,18 +35,6 @@ struct DeviceGuard {
   }
 };
 
-inline bool aligned(const void* p, uintptr_t a) {
-  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-// a*b without int64 overflow; false on overflow or negative operands.
-inline bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > LLONG_MAX / a) return false;
-  *out = a * b;
-  return true;
-}
-
 int bn_check(int dtype, int64_t B, int64_t C, int64_t HW, bool training, int64_t* M) {
   if (dtype != GBN_F32 && dtype != GBN_BF16) return GBN_EDTYPE;
   if (B < 0 || C < 0 || HW < 0) return GBN_EINVAL;
@@ -57,8 +45,6 @@ int bn_check(int dtype, int64_t B, int64_t C, int64_t HW, bool training, int64_t
   if (training && C > 0 && *M < 2) return GBN_EINVAL;
   return GBN_OK;
 }
-
-int to_status(cudaError_t e) { return e == cudaSuccess ? GBN_OK : GBN_ECUDA; }
 
 }  // namespace
 
@@ -522,14 +508,6 @@ int gbn_bn_nhwc_backward(const void* x, const void* dy, int dtype, int64_t M, in
 }
 
 // ------------------------------------------------------------ row-wise --
-
-static int row_check(int dtype, int64_t R, int64_t H) {
-  if (dtype != GBN_F32 && dtype != GBN_BF16) return GBN_EDTYPE;
-  if (R < 0 || H < 0 || H > INT32_MAX / 16) return GBN_EINVAL;
-  int64_t n;
-  if (!mul_ok(R, H, &n) || n > (LLONG_MAX >> 3)) return GBN_EINVAL;
-  return GBN_OK;
-}
 
 size_t gbn_rowwise_workspace_bytes(int64_t R, int64_t H, int kind, int dtype, int device) {
   if (row_check(dtype, R, H) != GBN_OK) return 0;

@@ -1,0 +1,157 @@
+// extern "C" entry points of the backbone-block operators (declared in
+// include/gbnorm.h): dropout with a counter-based mask, alone and inside
+// LayerNorm.  As in abi.cu, arguments are validated before CUDA is touched,
+// and every call only launches on the caller's stream.
+#include "gbn_internal.h"
+#include "philox.cuh"
+
+using namespace gbn;
+
+namespace {
+
+// p in [0, 1] (NaN refused); state 8-byte aligned (two 64-bit words).
+int rng_check(double p, const uint64_t* state) {
+  if (!(p >= 0.0 && p <= 1.0)) return GBN_EINVAL;
+  if (!aligned(state, 8)) return GBN_EALIGN;
+  return GBN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+// -------------------------------------------------------------- dropout --
+
+int gbn_dropout_forward(const void* x, int dtype, int64_t R, int64_t H, const void* bias,
+                        const void* residual, double p, uint64_t seed, uint64_t offset,
+                        const uint64_t* rng_state, void* y, void* stream) {
+  int rc = row_check(dtype, R, H);
+  if (rc != GBN_OK) return rc;
+  if ((rc = rng_check(p, rng_state)) != GBN_OK) return rc;
+  if (R == 0 || H == 0) return GBN_OK;
+  if (x == nullptr || y == nullptr) return GBN_EINVAL;
+  const DevInfo* dev = device_info(-1);
+  if (!dev) return GBN_ECUDA;
+  const bool fast_ok = aligned(x, 16) && aligned(bias, 16) && aligned(residual, 16) && aligned(y, 16);
+  const DropPlan plan = drop_plan(R, H, fast_ok, dtype, *dev);
+  return to_status(drop_forward(plan, dtype, x, bias, residual, y, R, H,
+                                make_rng(p, seed, offset, rng_state),
+                                static_cast<cudaStream_t>(stream)));
+}
+
+size_t gbn_dropout_workspace_bytes(int64_t R, int64_t H, int dtype, int device) {
+  if (row_check(dtype, R, H) != GBN_OK) return 0;
+  if (H == 0) return 256;
+  const DevInfo* dev = device_info(device);
+  if (!dev) return 0;
+  const DropPlan a = drop_plan(R, H, true, dtype, *dev), b = drop_plan(R, H, false, dtype, *dev);
+  return a.ws_bytes > b.ws_bytes ? a.ws_bytes : b.ws_bytes;
+}
+
+int gbn_dropout_backward(const void* dy, int dtype, int64_t R, int64_t H, double p, uint64_t seed,
+                         uint64_t offset, const uint64_t* rng_state, void* dx, void* dbias,
+                         void* ws, size_t ws_bytes, void* stream) {
+  int rc = row_check(dtype, R, H);
+  if (rc != GBN_OK) return rc;
+  if ((rc = rng_check(p, rng_state)) != GBN_OK) return rc;
+  if (H == 0 || (R == 0 && dbias == nullptr)) return GBN_OK;
+  if (R > 0 && (dy == nullptr || dx == nullptr)) return GBN_EINVAL;
+  if (dbias != nullptr && ws == nullptr) return GBN_EINVAL;
+  if (!aligned(ws, 16)) return GBN_EALIGN;
+  const DevInfo* dev = device_info(-1);
+  if (!dev) return GBN_ECUDA;
+  const DropPlan plan = drop_plan(R, H, aligned(dy, 16) && aligned(dx, 16), dtype, *dev);
+  if (dbias != nullptr && ws_bytes < plan.ws_bytes) return GBN_EWORKSPACE;
+  return to_status(drop_backward(plan, dtype, dy, dx, dbias, ws, R, H,
+                                 make_rng(p, seed, offset, rng_state),
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------- dropout in LayerNorm --
+
+int gbn_layernorm_dropout_forward(const void* input, int dtype, int64_t R, int64_t H,
+                                  const void* residual, const void* bias, double p, uint64_t seed,
+                                  uint64_t offset, const uint64_t* rng_state, const void* gamma,
+                                  const void* beta, float eps, void* y, void* z, float* mean,
+                                  float* rstd, void* stream) {
+  int rc = row_check(dtype, R, H);
+  if (rc != GBN_OK) return rc;
+  if ((rc = rng_check(p, rng_state)) != GBN_OK) return rc;
+  if (!(eps >= 0.f)) return GBN_EINVAL;
+  if (R == 0) return GBN_OK;
+  if (H == 0) return GBN_EINVAL;  // the mean over an empty row is undefined
+  if (input == nullptr || residual == nullptr || y == nullptr || mean == nullptr ||
+      rstd == nullptr)
+    return GBN_EINVAL;
+  const DevInfo* dev = device_info(-1);
+  if (!dev) return GBN_ECUDA;
+  const int64_t esize = dtype == GBN_F32 ? 4 : 2;
+  const bool vec_ok = (H * esize) % 16 == 0 && aligned(input, 16) && aligned(residual, 16) &&
+                      aligned(bias, 16) && aligned(gamma, 16) && aligned(beta, 16) &&
+                      aligned(y, 16) && aligned(z, 16);
+  const RngArgs rng = make_rng(p, seed, offset, rng_state);
+  RowFwdPtrs q;
+  q.x = input;
+  q.residual = residual;
+  q.bias = bias;
+  q.w = gamma;
+  q.beta = beta;
+  q.y = y;
+  q.z = z;
+  q.mean = mean;
+  q.rstd = rstd;
+  q.rng = &rng;
+  return to_status(row_fwd_launch(GBN_ROW_LN_FUSED, dtype, q, R, H, eps, 1.f, vec_ok, *dev,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+int gbn_layernorm_dropout_backward(const void* dy, const void* input_or_z, int dtype,
+                                   const float* mean, const float* rstd, const void* gamma,
+                                   int64_t R, int64_t H, const void* residual, const void* bias,
+                                   double p, uint64_t seed, uint64_t offset,
+                                   const uint64_t* rng_state, const float* dz_extra, void* dx,
+                                   void* dresidual, void* dgamma, void* dbeta, void* dbias,
+                                   void* ws, size_t ws_bytes, int flags, void* stream) {
+  int rc = row_check(dtype, R, H);
+  if (rc != GBN_OK) return rc;
+  if ((rc = rng_check(p, rng_state)) != GBN_OK) return rc;
+  if (flags & ~(GBN_LN_SAVED_Z | GBN_LN_DRES_F32)) return GBN_EINVAL;
+  const bool saved_z = (flags & GBN_LN_SAVED_Z) != 0;
+  if (saved_z && (residual || bias)) return GBN_EINVAL;  // z already holds them
+  if (H == 0) return GBN_OK;
+  if (gamma == nullptr || ws == nullptr) return GBN_EINVAL;
+  if (R > 0 && (dy == nullptr || input_or_z == nullptr || mean == nullptr || rstd == nullptr ||
+                dx == nullptr || (!saved_z && residual == nullptr)))
+    return GBN_EINVAL;
+  if (!aligned(ws, 16)) return GBN_EALIGN;
+  const DevInfo* dev = device_info(-1);
+  if (!dev) return GBN_ECUDA;
+  const bool fast_ok = aligned(dy, 16) && aligned(input_or_z, 16) && aligned(gamma, 16) &&
+                       aligned(dx, 16) && aligned(residual, 16) && aligned(bias, 16) &&
+                       aligned(dz_extra, 16) && aligned(dresidual, 16);
+  RowPlan plan;
+  if (!row_plan(R, H, GBN_ROW_LN_FUSED, dtype, fast_ok, false, dz_extra != nullptr, *dev, &plan))
+    return GBN_EINVAL;
+  if (ws_bytes < plan.ws_bytes) return GBN_EWORKSPACE;
+  const RngArgs rng = make_rng(p, seed, offset, rng_state);
+  LnPtrs q;
+  q.dy = dy;
+  q.x = input_or_z;
+  q.residual = residual;
+  q.bias = bias;
+  q.dz_extra = dz_extra;
+  q.mean = mean;
+  q.rstd = rstd;
+  q.gamma = gamma;
+  q.dx = dx;
+  q.dres = dresidual;
+  q.dgamma = dgamma;
+  q.dbeta = dbeta;
+  q.dbias = dbias;
+  q.saved_z = saved_z;
+  q.dres_f32 = (flags & GBN_LN_DRES_F32) != 0 && dtype != GBN_F32;
+  q.rng = &rng;
+  return to_status(ln_launch(plan, q, ws, dev->status, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -27,12 +27,21 @@
 // row whose mean is large next to its spread loses nothing to the rounding
 // of the mean (the same shifted form as the BatchNorm kernels).  Reductions
 // are fixed trees, so results are bit-deterministic.
+//
+// The fused form also runs with the counter-based mask of philox.cuh
+// (kRowLnRng): the same kernels, the mask bytes replaced by the generator's
+// bits, and a dropped element contributing exactly 0 whatever it holds.
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
+#include "philox.cuh"
 
 namespace gbn {
 
 namespace {
+
+// The fused LayerNorm whose mask is drawn (internal kind, next to GBN_ROW_*).
+constexpr int kRowLnRng = 3;
+template <int KIND> constexpr bool kFusedKind = KIND == GBN_ROW_LN_FUSED || KIND == kRowLnRng;
 
 struct FwdArgs {
   const void* x;         // RMSNorm x; LayerNorm input (fused: the dropout input)
@@ -50,6 +59,7 @@ struct FwdArgs {
   int32_t Hv;            // 16-byte vectors per row (vector kernels)
   float eps;
   float scale;           // dropout scale
+  RngArgs rng;           // kRowLnRng: the generator (its scale is `scale`)
 };
 
 constexpr int kThreads = 256;
@@ -88,7 +98,7 @@ template <typename T, int KIND, int KV>
 __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
   constexpr bool WARP = false;
   constexpr int VE = 16 / sizeof(T);
-  constexpr bool FUSED = KIND == GBN_ROW_LN_FUSED;
+  constexpr bool FUSED = kFusedKind<KIND>, RNG = KIND == kRowLnRng;
   using V = Vec<T, VE>;
   __shared__ float red[32];
   const int lane = threadIdx.x & 31;
@@ -103,6 +113,8 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
   const T* w = static_cast<const T*>(a.w);
   const T* beta = static_cast<const T*>(a.beta);
   const float invH = 1.f / (float)a.H;
+  Philox gen{};
+  if constexpr (RNG) gen = philox_load(a.rng);
 
   for (int64_t r = team; r < a.R; r += nteams) {
     const int64_t ro = r * (int64_t)a.H;
@@ -115,8 +127,9 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
         rx[k] = V::ld(x + ro + (int64_t)vi * VE);
         if constexpr (FUSED) {
           rr[k] = V::ld(res + ro + (int64_t)vi * VE);
-          mk[k] = a.mask ? load_mask<VE>(a.mask + ro + (int64_t)vi * VE)
-                         : make_uint2(0x01010101u, 0x01010101u);
+          if constexpr (!RNG)
+            mk[k] = a.mask ? load_mask<VE>(a.mask + ro + (int64_t)vi * VE)
+                           : make_uint2(0x01010101u, 0x01010101u);
         }
       }
     }
@@ -135,10 +148,18 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) bv[e] = 0.f;
           }
+          if constexpr (RNG) {
+            float f[VE];
+            keep_factors<VE>(gen, (uint64_t)(ro + (int64_t)vi * VE), a.rng.thr, a.scale, f);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const float keep = mask_byte(mk[k], e) ? a.scale : 0.f;
-            z[k][e] = fmaf(keep, z[k][e] + bv[e], rv[e]);
+            for (int e = 0; e < VE; ++e)
+              z[k][e] = fmaf(f[e] != 0.f ? z[k][e] + bv[e] : 0.f, f[e], rv[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+              const float keep = mask_byte(mk[k], e) ? a.scale : 0.f;
+              z[k][e] = fmaf(keep, z[k][e] + bv[e], rv[e]);
+            }
           }
         }
       } else {
@@ -226,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
 template <typename T, int KIND, int UNR>
 __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
   constexpr int VE = 16 / sizeof(T);
-  constexpr bool FUSED = KIND == GBN_ROW_LN_FUSED;
+  constexpr bool FUSED = kFusedKind<KIND>, RNG = KIND == kRowLnRng;
   using V = Vec<T, VE>;
   extern __shared__ __align__(16) float zsm[];
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5;
@@ -239,24 +260,34 @@ __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
   const T* w = static_cast<const T*>(a.w);
   const T* beta = static_cast<const T*>(a.beta);
   const float invH = 1.f / (float)a.H;
+  Philox gen{};
+  if constexpr (RNG) gen = philox_load(a.rng);
 
   auto zvec = [&](int64_t ro, int vi, float (&z)[VE]) {
     V::cvt(V::ld(x + ro + (int64_t)vi * VE), z);
     if constexpr (FUSED) {
       float rv[VE], bv[VE];
       V::cvt(V::ld(res + ro + (int64_t)vi * VE), rv);
-      const uint2 mk = a.mask ? load_mask<VE>(a.mask + ro + (int64_t)vi * VE)
-                              : make_uint2(0x01010101u, 0x01010101u);
+      uint2 mk = make_uint2(0x01010101u, 0x01010101u);
+      if (!RNG && a.mask) mk = load_mask<VE>(a.mask + ro + (int64_t)vi * VE);
       if (bias) {
         V::cvt(V::ld(bias + (int64_t)vi * VE), bv);
       } else {
 #pragma unroll
         for (int e = 0; e < VE; ++e) bv[e] = 0.f;
       }
+      if constexpr (RNG) {
+        float f[VE];
+        keep_factors<VE>(gen, (uint64_t)(ro + (int64_t)vi * VE), a.rng.thr, a.scale, f);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float keep = mask_byte(mk, e) ? a.scale : 0.f;
-        z[e] = fmaf(keep, z[e] + bv[e], rv[e]);
+        for (int e = 0; e < VE; ++e)
+          z[e] = fmaf(f[e] != 0.f ? z[e] + bv[e] : 0.f, f[e], rv[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const float keep = mask_byte(mk, e) ? a.scale : 0.f;
+          z[e] = fmaf(keep, z[e] + bv[e], rv[e]);
+        }
       }
     }
   };
@@ -346,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
 // row with stride blockDim (z is recomputed, the row is re-read from L2).
 template <typename T, int KIND>
 __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
-  constexpr bool FUSED = KIND == GBN_ROW_LN_FUSED;
+  constexpr bool FUSED = kFusedKind<KIND>, RNG = KIND == kRowLnRng;
   __shared__ float red[32];
   const int64_t H = a.H;
   const T* x = static_cast<const T*>(a.x);
@@ -355,9 +386,16 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   const T* w = static_cast<const T*>(a.w);
   const T* beta = static_cast<const T*>(a.beta);
   const float invH = 1.f / (float)a.H;
+  extern __shared__ __align__(16) uint8_t gbits[];
+  RowBits rb{a.H <= kRowBitsMaxH ? gbits : nullptr, 0};
+  Philox gen{};
+  if constexpr (RNG) gen = philox_load(a.rng);
   auto zval = [&](int64_t o, int64_t j) {
     float v = to_f32(x[o + j]);
-    if constexpr (FUSED) {
+    if constexpr (RNG) {
+      const bool keep = rowbits_keep(rb, gen, a.rng.thr, (uint64_t)(o + j));
+      v = fmaf(keep ? v + (bias ? to_f32(bias[j]) : 0.f) : 0.f, a.scale, to_f32(res[o + j]));
+    } else if constexpr (FUSED) {
       const float keep = (a.mask == nullptr || a.mask[o + j] != 0) ? a.scale : 0.f;
       v = fmaf(keep, v + (bias ? to_f32(bias[j]) : 0.f), to_f32(res[o + j]));
     }
@@ -365,6 +403,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   };
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
     const int64_t o = r * H;
+    if constexpr (RNG) rowbits_fill(rb, gen, a.rng.thr, (uint64_t)o, H);
     const float shift = KIND == GBN_ROW_RMS ? 0.f : zval(o, 0);
     float s = 0.f;
     for (int64_t j = threadIdx.x; j < H; j += blockDim.x) {
@@ -420,7 +459,8 @@ cudaError_t launch_kind(const FwdArgs& a, bool vec_ok, const DevInfo& dev, cudaS
     return launch(row_fwd_kernel<T, KIND, 4>, grid, block, 0, st, false, a);
   if (vec_ok && a.Hv <= 8 * kThreads)
     return launch(row_fwd_kernel<T, KIND, 8>, grid, block, 0, st, false, a);
-  return launch(row_fwd_generic_kernel<T, KIND>, grid, block, 0, st, false, a);
+  return launch(row_fwd_generic_kernel<T, KIND>, grid, block,
+                KIND == kRowLnRng ? rowbits_bytes(a.H) : 0, st, false, a);
 }
 
 template <typename T>
@@ -428,6 +468,7 @@ cudaError_t launch_typed(int kind, const FwdArgs& a, bool vec_ok, const DevInfo&
                          cudaStream_t st) {
   if (kind == GBN_ROW_RMS) return launch_kind<T, GBN_ROW_RMS>(a, vec_ok, dev, st);
   if (kind == GBN_ROW_LN) return launch_kind<T, GBN_ROW_LN>(a, vec_ok, dev, st);
+  if (kind == kRowLnRng) return launch_kind<T, kRowLnRng>(a, vec_ok, dev, st);
   return launch_kind<T, GBN_ROW_LN_FUSED>(a, vec_ok, dev, st);
 }
 
@@ -441,6 +482,9 @@ cudaError_t configure_unr(int bytes) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
     e = r;
   if ((r = cudaFuncSetAttribute(row_fwd_warp_kernel<T, GBN_ROW_LN_FUSED, UNR>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+    e = r;
+  if ((r = cudaFuncSetAttribute(row_fwd_warp_kernel<T, kRowLnRng, UNR>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
     e = r;
   return e;
@@ -481,6 +525,11 @@ cudaError_t row_fwd_launch(int kind, int dtype, const RowFwdPtrs& p, int64_t R, 
   a.Hv = (int32_t)(H * (dtype == GBN_F32 ? 4 : 2) / 16);
   a.eps = eps;
   a.scale = scale;
+  if (p.rng != nullptr) {
+    a.rng = *p.rng;
+    a.scale = p.rng->scale;
+    kind = kRowLnRng;
+  }
   return dtype == GBN_F32 ? launch_typed<float>(kind, a, vec_ok, dev, st)
                           : launch_typed<bf16>(kind, a, vec_ok, dev, st);
 }

@@ -26,6 +26,31 @@ struct DevInfo {
 // queried.  device < 0 means the current device.
 const DevInfo* device_info(int device);
 
+// ---- argument checks shared by the C entry points ----
+
+inline bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// a*b without int64 overflow; false on overflow or negative operands.
+inline bool mul_ok(int64_t a, int64_t b, int64_t* out) {
+  if (a < 0 || b < 0) return false;
+  if (a != 0 && b > INT64_MAX / a) return false;
+  *out = a * b;
+  return true;
+}
+
+inline int to_status(cudaError_t e) { return e == cudaSuccess ? GBN_OK : GBN_ECUDA; }
+
+// dtype and sizes of a row-wise call.
+inline int row_check(int dtype, int64_t R, int64_t H) {
+  if (dtype != GBN_F32 && dtype != GBN_BF16) return GBN_EDTYPE;
+  if (R < 0 || H < 0 || H > INT32_MAX / 16) return GBN_EINVAL;
+  int64_t n;
+  if (!mul_ok(R, H, &n) || n > (INT64_MAX >> 3)) return GBN_EINVAL;
+  return GBN_OK;
+}
+
 // Launch `kern` with the given configuration; `pdl` adds the programmatic
 // stream serialization attribute so the kernel may start while the
 // preceding kernel on the stream drains (it then calls griddepcontrol.wait).
@@ -204,6 +229,8 @@ struct RowPlan {
 constexpr int kLnRingWarpsKV1 = 14;
 constexpr int kLnRingWarpsKVn = 8;
 
+struct RngArgs;  // counter-based dropout mask (philox.cuh)
+
 struct LnPtrs {
   const void* dy = nullptr;
   const void* x = nullptr;
@@ -222,6 +249,7 @@ struct LnPtrs {
   void* dbias = nullptr;
   bool saved_z = false;   // x is the saved LayerNorm input z (fused outputs, no residual)
   bool dres_f32 = false;  // dres is fp32
+  const RngArgs* rng = nullptr;  // fused: the mask is drawn (mask null, scale unused)
 };
 
 // Plans the launch.  `fast_ok` says whether pointers/shape allow the
@@ -248,6 +276,7 @@ struct RowFwdPtrs {
   void* z = nullptr;
   float* mean = nullptr;
   float* rstd = nullptr;
+  const RngArgs* rng = nullptr;  // fused LayerNorm: the mask is drawn (mask null)
 };
 
 // kind: GBN_ROW_RMS, GBN_ROW_LN or GBN_ROW_LN_FUSED.  vec_ok: every tensor
@@ -271,6 +300,28 @@ cudaError_t row_kernels_configure(int smem_optin);
 // the library's bounded wait, for at most limit_ns; the expired wait sets
 // GBN_DEV_WAIT_TIMEOUT in *status.
 cudaError_t selftest_bounded_wait(int* status, uint64_t limit_ns, cudaStream_t st);
+
+// ------------------------------------------ dropout, mask never stored --
+
+constexpr int kDBlocksPerSm = 4;  // 256-thread blocks per SM the grid fills
+
+// Generator arguments for drop probability p in [0, 1].
+RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state);
+
+struct DropPlan {
+  bool fast = false;    // 8-element chunks per thread (else the tile kernel)
+  int64_t gx = 1;       // column tiles
+  int TX = 1, TY = 1;   // fast: chunks x rows of a block
+  int slices = 1;       // row slices (= rows of partial column sums)
+  size_t ws_bytes = 0;  // backward with dbias: the partials
+};
+// fast_ok: every tensor is 16-byte aligned.
+DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo& dev);
+cudaError_t drop_forward(const DropPlan& p, int dtype, const void* x, const void* bias,
+                         const void* res, void* y, int64_t R, int64_t H, const RngArgs& rng,
+                         cudaStream_t st);
+cudaError_t drop_backward(const DropPlan& p, int dtype, const void* dy, void* dx, void* dbias,
+                          void* ws, int64_t R, int64_t H, const RngArgs& rng, cudaStream_t st);
 
 // -------------------------------------------- BatchNorm, channels last --
 

@@ -32,10 +32,15 @@
 // are not whole 16-byte vectors, masks of rows that are not whole 16-byte
 // words, unaligned tensors, rows longer than the registers hold) run a plain
 // kernel followed by a separate fixed-order column-sum launch.
+//
+// With the counter-based mask (philox.cuh; MASK = kMaskRng) there are no mask
+// bytes to stage: each thread draws the block of its own vector, and a dropped
+// element contributes exactly 0 whatever its input holds.
 #include <type_traits>
 
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
+#include "philox.cuh"
 #include "row_engine.cuh"
 
 namespace gbn {
@@ -73,7 +78,13 @@ struct LnArgs {
   unsigned long long nonce;
   int32_t tprw;              // ring kernel: consumer warps per row slot
   int32_t rs;                // ring kernel: row slots
+  RngArgs rng;               // kMaskRng: the generator (its scale is `scale`)
 };
+
+// Where the fused kernels' keep decisions come from: mask bytes (or none:
+// everything kept), or the generator.
+constexpr int kMaskBytes = 0;
+constexpr int kMaskRng = 1;
 
 // One element's LayerNorm input z from the stage (fused: residual +
 // keep*(input + bias), exact (hi, lo) for fp32 outputs).
@@ -139,6 +150,26 @@ __device__ __forceinline__ void keep_pairs(uint2 m, float s, f2 (&keep2)[NP]) {
   }
 }
 
+// All-ones words where the generator keeps the element, else zero, for the NP
+// pairs of the 16-byte vector at element i.
+template <int NP>
+__device__ __forceinline__ void rng_pairs(const Philox& g, uint64_t i, uint32_t thr,
+                                          f2 (&keep2)[NP]) {
+  const uint4 w = philox_block(g, i >> 3);
+  uint32_t v[NP];
+  if constexpr (NP == 4) {
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  } else {
+    const bool second = (i & 4) != 0;
+    v[0] = second ? w.z : w.x;
+    v[1] = second ? w.w : w.y;
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    keep2[p] = f2_pack(__uint_as_float(keep_lo(v[p], thr) ? 0xffffffffu : 0u),
+                       __uint_as_float(keep_hi(v[p], thr) ? 0xffffffffu : 0u));
+}
+
 // Warp sums of four values at once (a transposed butterfly: 6 shuffles
 // instead of 20).  Lane l ends with the full sum of value ((l >> 4) & 1) * 2
 // + ((l >> 3) & 1); the addition order is fixed, so every lane holding a
@@ -165,8 +196,9 @@ constexpr int kLnRingWarps[3] = {0, kLnRingWarpsKV1, kLnRingWarpsKVn};
 // KV: 16-byte vectors per consumer thread and row; a stage holds RPS rows
 // (two for one-vector rows, else one).  MAXW: consumer warps at most (the
 // register budget of a thread follows from it).
-template <typename T, int KV, bool FUSED, int MAXW>
+template <typename T, int KV, bool FUSED, int MASK, int MAXW>
 __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs a) {
+  constexpr bool RNG = MASK == kMaskRng;
   constexpr int VE = 16 / sizeof(T);
   constexpr bool COMP = sizeof(T) == 4;
   using PK = Pairs16<T>;
@@ -187,7 +219,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
   const int NS = a.nstage;
   const int64_t H = a.H;
   const uint32_t rowb = (uint32_t)(H * sizeof(T));
-  const bool has_mask = FUSED && a.mask != nullptr;
+  const bool has_mask = FUSED && !RNG && a.mask != nullptr;
   const bool with_res = FUSED && !a.zin;
 
   const int P = (TPRW + 3) & ~3;  // padded warp run of a slot
@@ -223,6 +255,9 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
     const int ct = tid - 32, lane = ct & 31, cw = ct >> 5;
     const int grp = cw / TPRW, wis = cw - grp * TPRW, lr = ct - grp * TPR;
     epoch_read(sh, a.sync, ct);
+    Philox gen{};
+    if constexpr (RNG) gen = philox_load(a.rng);
+    const f2 scale2 = f2_splat(a.scale);
     const int gbar = 2 + grp;  // the group's named barrier
 
     // Per-column constants and accumulators of this thread's columns.  fp32
@@ -256,15 +291,24 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
     }
 
     // One 16-byte column vector as packed pairs: dy, z (fused: residual +
-    // keep*(input + bias)) and keep, from the raw words.
-    auto pairs = [&](int k, uint4 rdy, uint4 rx, uint4 rres, MaskRaw rm, f2 (&dy2)[NP],
-                     f2 (&z2)[NP], f2 (&keep2)[NP]) {
+    // keep*(input + bias)) and keep, from the raw words (kMaskRng: keep2 holds
+    // all-ones or zero words instead of factors).
+    auto pairs = [&](int k, uint64_t i0, uint4 rdy, uint4 rx, uint4 rres, MaskRaw rm,
+                     f2 (&dy2)[NP], f2 (&z2)[NP], f2 (&keep2)[NP]) {
       PK::get(rdy, dy2);
       f2 x2[NP];
       PK::get(rx, x2);
       if constexpr (FUSED) {
         f2 r2[NP];
         PK::get(rres, r2);
+        if constexpr (RNG) {
+          rng_pairs<NP>(gen, i0, a.rng.thr, keep2);
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            z2[p] = a.zin ? x2[p]
+                          : f2_fma(f2_add(x2[p], bia2[k][p]) & keep2[p], scale2, r2[p]);
+          return;
+        }
         if (has_mask) {
           uint2 m;
           if constexpr (VE == 8) m = rm;
@@ -286,14 +330,24 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
       }
     };
     // Scalar form for fp32 outputs: dy, exact z (hi, lo), keep.
-    auto elems = [&](int k, uint4 rdy, uint4 rx, uint4 rres, MaskRaw rm, float (&dyv)[VE],
-                     DF (&z)[VE], float (&keep)[VE]) {
+    auto elems = [&](int k, uint64_t i0, uint4 rdy, uint4 rx, uint4 rres, MaskRaw rm,
+                     float (&dyv)[VE], DF (&z)[VE], float (&keep)[VE]) {
       float xv[VE];
       Vec<T, VE>::cvt(rdy, dyv);
       Vec<T, VE>::cvt(rx, xv);
       if constexpr (FUSED) {
         float rv[VE];
         Vec<T, VE>::cvt(rres, rv);
+        if constexpr (RNG) {
+          keep_factors<VE>(gen, i0, a.rng.thr, a.scale, keep);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const bool on = keep[e] != 0.f;
+            z[e] = a.zin ? DF{xv[e], 0.f}
+                         : ln_z<FUSED, COMP>(on ? xv[e] : 0.f, rv[e], on ? bia[k][e] : 0.f, keep[e]);
+          }
+          return;
+        }
         uint32_t mk = 0xffu;
         if (has_mask) {
           uint32_t bits = 0;
@@ -394,7 +448,9 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
           f2 dy2[NP], z2[NP], keep2[NP];
-          pairs(k, rdy[q][k], rx[q][k], rres[q][k], rmk[q][k], dy2, z2, keep2);
+          const uint64_t i0 =
+              (uint64_t)((r0 + q) * H + (int64_t)min(lr + k * TPR, a.Hv - 1) * VE);
+          pairs(k, i0, rdy[q][k], rx[q][k], rres[q][k], rmk[q][k], dy2, z2, keep2);
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             const f2 xh2 = f2_mul(f2_sub(z2[p], mu2), rho2);
@@ -469,7 +525,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
             }
             float dyv[VE], keep[VE];
             DF z[VE];
-            elems(k, rdy[q][k], rx[q][k], rres[q][k], rmk[q][k], dyv, z, keep);
+            elems(k, (uint64_t)go, rdy[q][k], rx[q][k], rres[q][k], rmk[q][k], dyv, z, keep);
             float o_dz[VE], o_dx[VE];
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
@@ -480,7 +536,8 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
               const DF xm = df_mul(xh, mgx);
               inner = df_plus(DF{inner.hi, inner.lo - xm.lo}, -xm.hi);
               const DF dz = df_plus(df_mul(inner, rho[q]), dzx[e]);
-              const DF dxd = df_mul(dz, keep[e]);
+              DF dxd = df_mul(dz, keep[e]);
+              if (RNG && keep[e] == 0.f) dxd = DF{0.f, 0.f};
               o_dz[e] = df_round(dz);
               o_dx[e] = df_round(dxd);
               df_acc(acc_g[k][e], df_mul(xh, dyy));
@@ -505,7 +562,8 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
                 extra = f2_pack(t.x, t.y);
               }
               dz2[p] = f2_fma(inner, rho2, extra);
-              dx2[p] = FUSED ? f2_mul(dz2[p], kps[q][k][p]) : dz2[p];
+              if constexpr (RNG) dx2[p] = f2_mul(dz2[p], scale2) & kps[q][k][p];
+              else dx2[p] = FUSED ? f2_mul(dz2[p], kps[q][k][p]) : dz2[p];
               sg_g[k][p] = f2_fma(dy2[p], xh2, sg_g[k][p]);
               sg_b[k][p] = f2_add(sg_b[k][p], dy2[p]);
               if (FUSED) sg_x[k][p] = f2_add(sg_x[k][p], dx2[p]);
@@ -616,8 +674,13 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
 
 // Any H and alignment.  Block g owns rows g, g+G, ...; thread t owns columns
 // t, t+256, ...; column sums go straight into this block's partial rows.
-template <typename T, bool FUSED>
+template <typename T, bool FUSED, int MASK>
 __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
+  constexpr bool RNG = MASK == kMaskRng;
+  extern __shared__ __align__(16) uint8_t gbits[];
+  RowBits rb{a.H <= kRowBitsMaxH ? gbits : nullptr, 0};
+  Philox gen{};
+  if constexpr (RNG) gen = philox_load(a.rng);
   constexpr bool COMP = sizeof(T) == 4;
   __shared__ float red[2][2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
@@ -637,13 +700,17 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
     }
   // z (hi, lo): exact for fp32 outputs, plain fp32 otherwise
   auto zval = [&](int64_t r, int64_t j, float& keep) {
-    const float xv = to_f32(x[r * H + j]);
+    float xv = to_f32(x[r * H + j]);
     DF z{xv, 0.f};
     keep = 1.f;
     if constexpr (FUSED) {
-      keep = (a.mask == nullptr || a.mask[r * H + j] != 0) ? a.scale : 0.f;
+      if constexpr (RNG)
+        keep = rowbits_keep(rb, gen, a.rng.thr, (uint64_t)(r * H + j)) ? a.scale : 0.f;
+      else
+        keep = (a.mask == nullptr || a.mask[r * H + j] != 0) ? a.scale : 0.f;
       if (a.zin) return z;
-      const float b = bias ? to_f32(bias[j]) : 0.f;
+      float b = bias ? to_f32(bias[j]) : 0.f;
+      if (RNG && keep == 0.f) xv = b = 0.f;
       const float rv = to_f32(res[r * H + j]);
       if constexpr (COMP) {
         const DF kt = df_mul(two_sum(xv, b), keep);
@@ -667,6 +734,7 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
   int it = 0;
   for (int64_t r = g; r < a.R; r += G, ++it) {
     const float mu = a.mean[r], rho = a.rstd[r];
+    if constexpr (RNG) rowbits_fill(rb, gen, a.rng.thr, (uint64_t)(r * H), H);
     float sg = 0.f, sgx = 0.f;
     for (int64_t j = tid; j < H; j += blockDim.x) {
       float keep;
@@ -695,7 +763,8 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
         const DF xm = df_mul(xh, mgx);
         inner = df_plus(DF{inner.hi, inner.lo - xm.lo}, -xm.hi);
         const DF dz = df_plus(df_mul(inner, rho), zx);
-        const DF dxd = df_mul(dz, FUSED ? keep : 1.f);
+        DF dxd = df_mul(dz, FUSED ? keep : 1.f);
+        if (RNG && keep == 0.f) dxd = DF{0.f, 0.f};
         static_cast<T*>(a.dx)[r * H + j] = from_f32<T>(df_round(dxd));
         if (FUSED && a.dres != nullptr) static_cast<T*>(a.dres)[r * H + j] = from_f32<T>(df_round(dz));
         DF d{P(0, 0)[j], P(0, 1)[j]};
@@ -712,7 +781,7 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
       } else {
         const float xh = (z.hi - mu) * rho;
         const float dz = fmaf(rho, dyy * gm - mg - xh * mgx, zx);
-        const float dxv = FUSED ? dz * keep : dz;
+        const float dxv = FUSED ? (RNG && keep == 0.f ? 0.f : dz * keep) : dz;
         static_cast<T*>(a.dx)[r * H + j] = from_f32<T>(dxv);
         if (FUSED && a.dres != nullptr) {
           if (a.dres_f32) static_cast<float*>(a.dres)[r * H + j] = dz;
@@ -727,7 +796,7 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
   pdl_launch_dependents();
 }
 
-template <typename T, int KV, bool FUSED>
+template <typename T, int KV, bool FUSED, int MASK>
 cudaError_t launch_ring(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.G);
@@ -739,27 +808,30 @@ cudaError_t launch_ring(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ln_bwd_ring_kernel<T, KV, FUSED, kLnRingWarps[KV]>, a);
+  return cudaLaunchKernelEx(&cfg, ln_bwd_ring_kernel<T, KV, FUSED, MASK, kLnRingWarps[KV]>, a);
 }
 
 // Ring instances: KV = 1 (at most 14 consumer warps) and, for bf16, KV = 2
 // (at most 8), the counts the plan uses.
-template <typename T, bool FUSED>
+template <typename T, bool FUSED, int MASK = kMaskBytes>
 cudaError_t launch_typed(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
   if (!p.fast)
-    return launch(ln_bwd_generic_kernel<T, FUSED>, dim3(p.G), dim3(p.threads), 0, st, false, a);
+    return launch(ln_bwd_generic_kernel<T, FUSED, MASK>, dim3(p.G), dim3(p.threads),
+                  MASK == kMaskRng ? rowbits_bytes(a.H) : 0, st, false, a);
   if constexpr (sizeof(T) == 2)
-    if (p.kv == 2) return launch_ring<T, 2, FUSED>(p, a, st);
-  return launch_ring<T, 1, FUSED>(p, a, st);
+    if (p.kv == 2) return launch_ring<T, 2, FUSED, MASK>(p, a, st);
+  return launch_ring<T, 1, FUSED, MASK>(p, a, st);
 }
 
 template <typename T, int KV>
 cudaError_t set_smem(int bytes) {
-  cudaError_t e1 = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, true, kLnRingWarps[KV]>,
+  cudaError_t e1 = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, true, kMaskBytes, kLnRingWarps[KV]>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  cudaError_t e2 = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, false, kLnRingWarps[KV]>,
+  cudaError_t e2 = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, false, kMaskBytes, kLnRingWarps[KV]>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e1 != cudaSuccess ? e1 : e2;
+  cudaError_t e3 = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, true, kMaskRng, kLnRingWarps[KV]>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : e3);
 }
 
 template <typename T>
@@ -821,7 +893,12 @@ cudaError_t ln_launch(const RowPlan& p, const LnPtrs& q, void* ws, int* status,
   a.tprw = p.tprw;
   a.rs = p.rs;
   cudaError_t e;
-  if (p.dtype == GBN_F32)
+  if (q.rng != nullptr) {
+    a.rng = *q.rng;
+    a.scale = q.rng->scale;
+    e = p.dtype == GBN_F32 ? launch_typed<float, true, kMaskRng>(p, a, st)
+                           : launch_typed<bf16, true, kMaskRng>(p, a, st);
+  } else if (p.dtype == GBN_F32)
     e = fused ? launch_typed<float, true>(p, a, st) : launch_typed<float, false>(p, a, st);
   else
     e = fused ? launch_typed<bf16, true>(p, a, st) : launch_typed<bf16, false>(p, a, st);

@@ -52,6 +52,8 @@ _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_U64 = ctypes.c_uint64
+_D = ctypes.c_double
 
 _SIGNATURES = {
     "gbn_abi_version": (_INT, []),
@@ -99,6 +101,15 @@ _SIGNATURES = {
     "gbn_rmsnorm_forward": (_INT, [_P, _P, _INT, _I64, _I64, _F, _P, _P, _P]),
     "gbn_layernorm_forward": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P, _F, _P, _P, _F, _P, _P,
                                      _P, _P, _P]),
+    "gbn_dropout_forward": (_INT, [_P, _INT, _I64, _I64, _P, _P, _D, _U64, _U64, _P, _P, _P]),
+    "gbn_dropout_workspace_bytes": (_SZ, [_I64, _I64, _INT, _INT]),
+    "gbn_dropout_backward": (_INT, [_P, _INT, _I64, _I64, _D, _U64, _U64, _P, _P, _P, _P, _SZ,
+                                    _P]),
+    "gbn_layernorm_dropout_forward": (_INT, [_P, _INT, _I64, _I64, _P, _P, _D, _U64, _U64, _P, _P,
+                                             _P, _F, _P, _P, _P, _P, _P]),
+    "gbn_layernorm_dropout_backward": (_INT, [_P, _P, _INT, _P, _P, _P, _I64, _I64, _P, _P, _D,
+                                              _U64, _U64, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
+                                              _INT, _P]),
 }
 
 
@@ -671,3 +682,159 @@ def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, *, residual=None, bias
             _ptr(mean), _ptr(rstd), _stream(x.device))
     _check("gbn_layernorm_forward", st)
     return {"y": y, "z": z, "mean": mean, "rstd": rstd}
+
+
+# ------------------------------------------- dropout, mask never stored --
+
+def _rng(rng, ref):
+    """(seed, offset, rng_state) of a dropout call: ``rng`` is a pair of
+    Python ints (taken modulo 2**64), or a CUDA int64 tensor of two elements
+    (seed, offset) that the kernels read when they run."""
+    if isinstance(rng, torch.Tensor):
+        if _cuda(rng, "rng").dtype != torch.int64 or rng.numel() != 2:
+            raise TypeError("rng must be an int64 tensor (seed, offset) or a pair of ints")
+        _same_device(ref, ("rng", rng))
+        return 0, 0, _ptr(rng)
+    seed, offset = rng
+    return int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFFFFFFFFFF, None
+
+
+def _like(t, ref, name):
+    if _cuda(t, name).shape != ref.shape or t.dtype != ref.dtype:
+        raise ValueError(f"{name} must match in shape and dtype")
+    return t
+
+
+def _col_vec(t, ref, H, name):
+    if t is not None and (_cuda(t, name).dtype != ref.dtype or t.numel() != H):
+        raise ValueError(f"{name} must match the rows' dtype and last dimension")
+
+
+def dropout_forward(x, p, rng, *, bias=None, residual=None, y=None):
+    """``y = residual + keep*s*(x + bias)`` over the rows of a contiguous
+    [..., H] tensor; the mask comes from the counter-based generator of
+    ``rng`` = (seed, offset) (see gbn_dropout_forward) and is not stored.
+    The backward draws it again from the same ``rng``."""
+    R, H = _rows(x, "x")
+    _col_vec(bias, x, H, "bias")
+    if residual is not None:
+        _like(residual, x, "residual")
+    y = torch.empty_like(x) if y is None else _like(y, x, "y")
+    _same_device(x, ("bias", bias), ("residual", residual), ("y", y))
+    seed, offset, state = _rng(rng, x)
+    with torch.cuda.device(x.device):
+        st = lib().gbn_dropout_forward(_ptr(x), _code(x.dtype), R, H, _ptr(bias), _ptr(residual),
+                                       float(p), seed, offset, state, _ptr(y), _stream(x.device))
+    _check("gbn_dropout_forward", st)
+    return y
+
+
+def dropout_workspace(dy):
+    R, H = _rows(dy, "dy")
+    with torch.cuda.device(dy.device):
+        n = lib().gbn_dropout_workspace_bytes(R, H, _code(dy.dtype), -1)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=dy.device)
+
+
+def dropout_backward(dy, p, rng, *, want_dbias=False, dx=None, dbias=None, ws=None):
+    """Backward of ``dropout_forward`` for the same ``p`` and ``rng``.
+    Returns (dx, dbias); dbias is None unless wanted (or given).  The
+    residual's gradient is dy itself."""
+    R, H = _rows(dy, "dy")
+    dx = torch.empty_like(dy) if dx is None else _like(dx, dy, "dx")
+    if dbias is None and want_dbias:
+        dbias = torch.empty(H, dtype=dy.dtype, device=dy.device)
+    _col_vec(dbias, dy, H, "dbias")
+    if dbias is not None and ws is None:
+        ws = dropout_workspace(dy)
+    _same_device(dy, ("dx", dx), ("dbias", dbias), ("ws", ws))
+    seed, offset, state = _rng(rng, dy)
+    with torch.cuda.device(dy.device):
+        st = lib().gbn_dropout_backward(
+            _ptr(dy), _code(dy.dtype), R, H, float(p), seed, offset, state, _ptr(dx), _ptr(dbias),
+            _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(dy.device))
+    _check("gbn_dropout_backward", st)
+    return dx, dbias
+
+
+def layernorm_dropout_forward(x, residual, p, rng, gamma=None, beta=None, eps=1e-5, *, bias=None,
+                              y=None, z=None, mean=None, rstd=None, want_z=True):
+    """``layernorm_forward`` fused with bias+dropout+add, the mask drawn from
+    ``rng`` (see ``dropout_forward``): z = residual + keep*s*(x + bias), y =
+    LayerNorm(z).  Returns a dict with y, z (None when not wanted), mean,
+    rstd."""
+    R, H = _rows(x, "x")
+    _like(residual, x, "residual")
+    for name, t in (("gamma", gamma), ("beta", beta), ("bias", bias)):
+        _col_vec(t, x, H, name)
+    y = torch.empty_like(x) if y is None else _like(y, x, "y")
+    if z is None and want_z:
+        z = torch.empty_like(x)
+    if z is not None:
+        _like(z, x, "z")
+    mean = torch.empty(R, dtype=torch.float32, device=x.device) if mean is None else mean
+    rstd = torch.empty(R, dtype=torch.float32, device=x.device) if rstd is None else rstd
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if _cuda(t, name).dtype != torch.float32 or t.numel() != R:
+            raise TypeError(f"{name} must be float32 with one value per row")
+    _same_device(x, ("residual", residual), ("gamma", gamma), ("beta", beta), ("bias", bias),
+                 ("y", y), ("z", z), ("mean", mean), ("rstd", rstd))
+    seed, offset, state = _rng(rng, x)
+    with torch.cuda.device(x.device):
+        st = lib().gbn_layernorm_dropout_forward(
+            _ptr(x), _code(x.dtype), R, H, _ptr(residual), _ptr(bias), float(p), seed, offset,
+            state, _ptr(gamma), _ptr(beta), float(eps), _ptr(y), _ptr(z), _ptr(mean), _ptr(rstd),
+            _stream(x.device))
+    _check("gbn_layernorm_dropout_forward", st)
+    return {"y": y, "z": z, "mean": mean, "rstd": rstd}
+
+
+def layernorm_dropout_backward(dy, x, residual, mean, rstd, gamma, p, rng, *, bias=None,
+                               dz_extra=None, dx=None, dresidual=None, dgamma=None, dbeta=None,
+                               dbias=None, ws=None, want_dbias=True, saved_z=False,
+                               dres_f32=False):
+    """Backward of ``layernorm_dropout_forward`` for the same ``p`` and
+    ``rng``; with ``saved_z``, ``x`` is the forward's z and ``residual`` (and
+    ``bias``) None.  ``dz_extra`` and ``dres_f32`` as in
+    ``layernorm_backward``.  Returns a dict with dx, dresidual, dgamma, dbeta,
+    dbias."""
+    R, H = _rows(x, "x")
+    _like(dy, x, "dy")
+    if residual is not None:
+        _like(residual, x, "residual")
+    elif not saved_z:
+        raise ValueError("residual is required (or saved_z, with x the saved z)")
+    for name, t in (("gamma", gamma), ("bias", bias), ("dgamma", dgamma), ("dbeta", dbeta),
+                    ("dbias", dbias)):
+        _col_vec(t, x, H, name)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if _cuda(t, name).dtype != torch.float32 or t.numel() != R:
+            raise TypeError(f"{name} must be float32 with one value per row")
+    if dz_extra is not None and (_cuda(dz_extra, "dz_extra").dtype != torch.float32
+                                 or dz_extra.numel() != x.numel()):
+        raise TypeError("dz_extra must be float32, one value per element")
+    res_dtype = torch.float32 if dres_f32 else x.dtype
+    dx = torch.empty_like(x) if dx is None else _like(dx, x, "dx")
+    if dresidual is None:
+        dresidual = torch.empty_like(x, dtype=res_dtype)
+    elif _cuda(dresidual, "dresidual").shape != x.shape or dresidual.dtype != res_dtype:
+        raise ValueError("dresidual must match x (float32 with dres_f32)")
+    dgamma = torch.empty_like(gamma) if dgamma is None else dgamma
+    dbeta = torch.empty_like(gamma) if dbeta is None else dbeta
+    if dbias is None and want_dbias:
+        dbias = torch.empty_like(gamma)
+    ws = rowwise_workspace(R, H, GBN_ROW_LN_FUSED, x.dtype, x.device) if ws is None else ws
+    _same_device(x, ("dy", dy), ("residual", residual), ("mean", mean), ("rstd", rstd),
+                 ("gamma", gamma), ("bias", bias), ("dz_extra", dz_extra), ("dx", dx),
+                 ("dresidual", dresidual), ("dgamma", dgamma), ("dbeta", dbeta),
+                 ("dbias", dbias), ("ws", ws))
+    seed, offset, state = _rng(rng, x)
+    flags = (GBN_LN_SAVED_Z if saved_z else 0) | (GBN_LN_DRES_F32 if dres_f32 else 0)
+    with torch.cuda.device(x.device):
+        st = lib().gbn_layernorm_dropout_backward(
+            _ptr(dy), _ptr(x), _code(x.dtype), _ptr(mean), _ptr(rstd), _ptr(gamma), R, H,
+            _ptr(residual), _ptr(bias), float(p), seed, offset, state, _ptr(dz_extra), _ptr(dx),
+            _ptr(dresidual), _ptr(dgamma), _ptr(dbeta), _ptr(dbias), _ptr(ws),
+            ws.numel() * ws.element_size(), flags, _stream(x.device))
+    _check("gbn_layernorm_dropout_backward", st)
+    return {"dx": dx, "dresidual": dresidual, "dgamma": dgamma, "dbeta": dbeta, "dbias": dbias}

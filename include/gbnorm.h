@@ -475,6 +475,67 @@ GBN_API int gbn_layernorm_forward(const void* x_or_input, int dtype, int64_t R, 
                                   const void* gamma, const void* beta, float eps, void* y,
                                   void* z, float* mean, float* rstd, void* stream);
 
+/* =========================================================================
+ * Dropout from a counter-based generator: the mask is drawn where it is used
+ * and never stored.
+ *
+ * Generator: Philox4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw, "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011).  Element i = r*H + h takes the
+ * 16-bit piece i mod 8 (low half of word 0, high half of word 0, low half of
+ * word 1, ...) of the four words of block i / 8, with the 128-bit counter
+ * (block, offset) and the key seed.  It is kept iff the piece is below
+ * T = floor((1 - p)*2^16 + 1/2), and a kept element is multiplied by
+ * s = 2^16 / T: the drop probability is p rounded to a multiple of 2^-16, and
+ * the expectation is exact for the rounded one.  p = 0 keeps everything, p = 1
+ * nothing.  A dropped element contributes exactly 0, infinities and NaNs too.
+ *
+ * (seed, offset) come from the arguments, or, where rng_state is non-NULL,
+ * from the two 64-bit words rng_state[0], rng_state[1] in device memory, read
+ * when the kernels run: a captured graph then draws other masks once they are
+ * changed between replays.  The same (seed, offset) gives the backward the
+ * forward's mask; steps and call sites take offsets of their own.  Bits do not
+ * depend on dtype, alignment or launch shape.
+ * p outside [0, 1]: GBN_EINVAL; rng_state not 8-byte aligned: GBN_EALIGN.
+ * ======================================================================= */
+
+/* y = residual + keep*s*(x + bias) over [R, H] rows; bias [H] and residual
+ * [R, H] may be NULL.  y may alias x or residual.                           */
+GBN_API int gbn_dropout_forward(const void* x, int dtype, int64_t R, int64_t H,
+                                const void* bias, const void* residual, double p,
+                                uint64_t seed, uint64_t offset, const uint64_t* rng_state,
+                                void* y, void* stream);
+
+/* Workspace bytes of gbn_dropout_backward with dbias (-1: current device).  */
+GBN_API size_t gbn_dropout_workspace_bytes(int64_t R, int64_t H, int dtype, int device);
+
+/* dx = keep*s*dy; dbias[h] = sum_r dx[r, h] (in `dtype`) unless dbias is
+ * NULL (then ws may be NULL too).  The residual's gradient is dy itself.
+ * dx may alias dy.                                                          */
+GBN_API int gbn_dropout_backward(const void* dy, int dtype, int64_t R, int64_t H, double p,
+                                 uint64_t seed, uint64_t offset, const uint64_t* rng_state,
+                                 void* dx, void* dbias, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* gbn_layernorm_forward, fused form, with the drawn mask in place of the mask
+ * bytes and the dropout scale: z = residual + keep*s*(input + bias) ...  The
+ * outputs and the optional arguments are the same.                          */
+GBN_API int gbn_layernorm_dropout_forward(const void* input, int dtype, int64_t R, int64_t H,
+                                          const void* residual, const void* bias, double p,
+                                          uint64_t seed, uint64_t offset,
+                                          const uint64_t* rng_state, const void* gamma,
+                                          const void* beta, float eps, void* y, void* z,
+                                          float* mean, float* rstd, void* stream);
+
+/* gbn_layernorm_backward_ex, fused form, with the drawn mask.  residual is
+ * required unless flags has GBN_LN_SAVED_Z.  ws: at least
+ * gbn_rowwise_workspace_bytes(R, H, GBN_ROW_LN_FUSED, dtype, -1) bytes.     */
+GBN_API int gbn_layernorm_dropout_backward(
+    const void* dy, const void* input_or_z, int dtype, const float* mean, const float* rstd,
+    const void* gamma, int64_t R, int64_t H, const void* residual, const void* bias, double p,
+    uint64_t seed, uint64_t offset, const uint64_t* rng_state, const float* dz_extra, void* dx,
+    void* dresidual, void* dgamma, void* dbeta, void* dbias, void* ws, size_t ws_bytes,
+    int flags, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,7 +8,8 @@ imports it, and the two share no code: no kernels, helpers, constants or
 pre/post-processing.  Inputs are the exact stored values widened to float64;
 nothing is rounded to a storage type inside the oracle.
 
-Every function is written from the pages it cites and pinned by the
+Every function is written from the pages (or the published method) it cites
+and pinned by the
 ``-m "not gpu"`` tests in ``tests/test_oracle_pins.py`` against things other
 than itself: PyTorch float64 autograd (an independent implementation),
 central finite differences, closed-form invariants and exact rational
@@ -39,6 +40,14 @@ from .layernorm import (
     fused_bias_dropout_add_layer_norm_backward,
     layer_norm_backward_saved_z,
 )
+from .dropout import (
+    philox4x32_10,
+    dropout_threshold,
+    dropout_scale,
+    dropout_mask,
+    dropout_forward,
+    dropout_backward,
+)
 
 __all__ = [
     "batch_norm_forward_train",
@@ -60,4 +69,10 @@ __all__ = [
     "layer_norm_backward",
     "fused_bias_dropout_add_layer_norm_backward",
     "layer_norm_backward_saved_z",
+    "philox4x32_10",
+    "dropout_threshold",
+    "dropout_scale",
+    "dropout_mask",
+    "dropout_forward",
+    "dropout_backward",
 ]
