@@ -1,0 +1,373 @@
+"""Dropout from the counter-based generator, alone and inside LayerNorm: the
+generator against its published vectors, refusals, and the CUDA path against
+the float64 oracle at the sizes, alignments and values where it can go wrong.
+
+Tolerances are those of every parity test (tests/tolerances.py): fp32 outputs
+take one FMA and a sum with carried errors, bf16 outputs one rounding of an
+fp32 value (half a step, of the two steps allowed) and, in the column sums,
+fp32 additions far below it.  Masks are compared exactly."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+from . import tolerances as tol
+
+DEV = "cuda:0"
+OK, EINVAL, EDTYPE, EALIGN, EWORKSPACE = 0, -1, -2, -3, -4
+P = ctypes.c_void_p
+A16, A4 = P(0x10000), P(0x10004)
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+SEED, OFFSET = 0x9E3779B97F4A7C15, (7 << 32) + 11
+
+
+# ------------------------------------------------------------- the oracle
+
+@pytest.mark.parametrize("counter,key,words", [
+    ((0,) * 4, (0,) * 2, (0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8)),
+    ((0xFFFFFFFF,) * 4, (0xFFFFFFFF,) * 2, (0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD)),
+    ((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0),
+     (0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1)),
+])
+def test_generator_known_answers(counter, key, words):
+    assert oracle.philox4x32_10(counter, key) == words
+
+
+def test_oracle_mask_is_unbiased_and_placed():
+    n = 40000
+    for p in (0.1, 0.5):
+        m = oracle.dropout_mask(n, p, SEED, OFFSET)
+        kept = oracle.dropout_threshold(p) / 65536.0
+        assert abs(m.mean() - kept) < 5 * np.sqrt(kept * (1 - kept) / n)
+    a = oracle.dropout_mask(100, 0.3, SEED, OFFSET)
+    assert np.array_equal(a[13:60], oracle.dropout_mask(47, 0.3, SEED, OFFSET, start=13))
+    assert oracle.dropout_mask(64, 0.0, 1, 2).all()
+    assert not oracle.dropout_mask(64, 1.0, 1, 2).any()
+    assert oracle.dropout_scale(1.0) == 0.0
+
+
+def test_oracle_backward_matches_differences():
+    g = np.random.default_rng(3)
+    x, b, r, c = g.normal(size=(5, 6)), g.normal(size=6), g.normal(size=(5, 6)), g.normal(size=(5, 6))
+
+    def loss(xx, bb):
+        return (oracle.dropout_forward(xx, 0.4, 5, 6, bb, r) * c).sum()
+
+    bw = oracle.dropout_backward(c, 0.4, 5, 6)
+    h = 1e-6
+    for i in range(5):
+        for j in range(6):
+            e = np.zeros_like(x)
+            e[i, j] = h
+            assert abs((loss(x + e, b) - loss(x - e, b)) / (2 * h) - bw["dx"][i, j]) < 1e-6
+    for j in range(6):
+        e = np.zeros_like(b)
+        e[j] = h
+        assert abs((loss(x, b + e) - loss(x, b - e)) / (2 * h) - bw["dbias"][j]) < 1e-6
+
+
+# --------------------------------------------------------------- refusals
+
+def test_argument_errors(gbn):
+    L = gbn.lib()
+
+    def fwd(x=A16, dtype=0, R=4, H=8, bias=None, res=None, p=0.1, state=None, y=A16):
+        return L.gbn_dropout_forward(x, dtype, R, H, bias, res, p, 1, 2, state, y, None)
+
+    assert fwd(dtype=5) == EDTYPE
+    for kw in ({"x": None}, {"y": None}, {"R": -1}, {"H": -1}, {"H": 1 << 30}, {"p": -0.01},
+               {"p": 1.01}, {"p": float("nan")}, {"R": 1 << 60, "H": 1 << 20}):
+        assert fwd(**kw) == EINVAL, kw
+    assert fwd(state=A4) == EALIGN
+    assert fwd(R=0, x=None, y=None) == OK
+    assert fwd(H=0) == OK
+
+    def bwd(dy=A16, dtype=0, R=4, H=8, p=0.1, state=None, dx=A16, db=A16, ws=A16, n=1 << 20):
+        return L.gbn_dropout_backward(dy, dtype, R, H, p, 1, 2, state, dx, db, ws, n, None)
+
+    assert bwd(dtype=-1) == EDTYPE
+    for kw in ({"dy": None}, {"dx": None}, {"ws": None}, {"p": 2.0}, {"R": -3}):
+        assert bwd(**kw) == EINVAL, kw
+    assert bwd(ws=A4) == EALIGN
+    assert bwd(state=A4) == EALIGN
+    assert bwd(R=0, db=None) == OK
+
+
+def test_layernorm_argument_errors(gbn):
+    L = gbn.lib()
+
+    def fwd(x=A16, dtype=0, R=4, H=8, res=A16, p=0.1, eps=1e-5, y=A16, mean=A16, rstd=A16):
+        return L.gbn_layernorm_dropout_forward(x, dtype, R, H, res, None, p, 1, 2, None, None,
+                                               None, eps, y, None, mean, rstd, None)
+
+    assert fwd(dtype=9) == EDTYPE
+    for kw in ({"x": None}, {"res": None}, {"y": None}, {"mean": None}, {"rstd": None},
+               {"p": 1.5}, {"eps": -1.0}, {"eps": float("nan")}, {"H": 0}):
+        assert fwd(**kw) == EINVAL, kw
+    assert fwd(R=0) == OK
+
+    def bwd(dy=A16, x=A16, gamma=A16, R=4, H=8, res=A16, bias=None, p=0.1, dx=A16, ws=A16,
+            flags=0):
+        return L.gbn_layernorm_dropout_backward(dy, x, 0, A16, A16, gamma, R, H, res, bias, p, 1,
+                                                2, None, None, dx, None, None, None, None, ws,
+                                                1 << 20, flags, None)
+
+    for kw in ({"dy": None}, {"x": None}, {"gamma": None}, {"res": None}, {"dx": None},
+               {"ws": None}, {"p": -1.0}, {"flags": 8}, {"flags": 1}):
+        assert bwd(**kw) == EINVAL, kw
+    assert bwd(res=None, bias=A16, flags=1) == EINVAL
+    assert bwd(ws=A4) == EALIGN
+
+
+def test_binding_refusals(gbn):
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError):
+        gbn.dropout_forward(x, 0.1, (1, 2))        # not a CUDA tensor
+    with pytest.raises(ValueError):
+        gbn.layernorm_dropout_forward(x, x, 0.1, (1, 2))
+
+
+# ----------------------------------------------------------------- the GPU
+
+@pytest.fixture
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return DEV
+
+
+def _f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def _rand(shape, dtype, seed, mis=False):
+    """Seeded N(0, 1); `mis`: a view one element off 16-byte alignment."""
+    g = torch.Generator().manual_seed(seed)
+    t = torch.randn(shape, generator=g).to(DT[dtype])
+    if not mis:
+        return t.to(DEV)
+    big = torch.zeros(t.numel() + 1, dtype=t.dtype, device=DEV)
+    big[1:] = t.reshape(-1).to(DEV)
+    return big[1:].view(shape)
+
+
+SHAPES = [(1, 1), (1, 7), (3, 8), (2, 16), (5, 40), (17, 1001), (64, 248), (9, 249), (1, 4096),
+          (300, 24), (2, 2056), (33, 63)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,H", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_forward(gbn, dev, R, H, dtype):
+    for k, (bias, res, mis) in enumerate([(True, True, False), (False, False, False),
+                                          (True, False, True), (False, True, False)]):
+        x = _rand((R, H), dtype, 3 + k, mis)
+        b = _rand((H,), dtype, 13 + k) if bias else None
+        r = _rand((R, H), dtype, 23 + k) if res else None
+        p = (0.1, 0.37, 0.5, 0.0)[k]
+        y = gbn.dropout_forward(x, p, (SEED, OFFSET + k), bias=b, residual=r)
+        ref = oracle.dropout_forward(_f64(x), p, SEED, OFFSET + k, _f64(b), _f64(r))
+        tol.check(y, ref, f"dropout {R}x{H} {dtype} {k}", dtype)
+        if r is None:
+            keep = oracle.dropout_mask(R * H, p, SEED, OFFSET + k).reshape(R, H)
+            assert not np.any(_f64(y)[~keep])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,H", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward(gbn, dev, R, H, dtype):
+    for mis in (False, True):
+        dy = _rand((R, H), dtype, 5, mis)
+        dx, db = gbn.dropout_backward(dy, 0.25, (SEED, OFFSET), want_dbias=True)
+        ref = oracle.dropout_backward(_f64(dy), 0.25, SEED, OFFSET)
+        tol.check(dx, ref["dx"], f"dx {R}x{H} {dtype}", dtype)
+        tol.check(db, ref["dbias"], f"dbias {R}x{H} {dtype}", dtype)
+        dx2, none = gbn.dropout_backward(dy, 0.25, (SEED, OFFSET))
+        assert none is None and torch.equal(dx, dx2)
+
+
+@pytest.mark.gpu
+def test_mask_does_not_depend_on_type_or_alignment(gbn, dev):
+    ones = torch.ones(21, 136, device=dev)
+    ref = oracle.dropout_mask(21 * 136, 0.3, 12, 34).reshape(21, 136)
+    for t in (ones, ones.bfloat16(), _rand((21, 136), "f32", 1, True).fill_(1.0)):
+        y = gbn.dropout_forward(t, 0.3, (12, 34))
+        assert np.array_equal(_f64(y) != 0, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("p,H", [(0.0, 40), (1.0, 40), (1.0, 41), (1e-6, 40), (0.99999, 41)])
+def test_extreme_probabilities(gbn, dev, p, H):
+    x = _rand((6, H), "f32", 9)
+    y = gbn.dropout_forward(x, p, (3, 4))
+    tol.check_f32(y, oracle.dropout_forward(_f64(x), p, 3, 4), f"p={p}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [64, 61])
+def test_dropped_infinities_and_nans_leave_nothing(gbn, dev, H):
+    keep = torch.from_numpy(oracle.dropout_mask(8 * H, 0.5, 21, 22).reshape(8, H)).to(dev)
+    for dtype in ("f32", "bf16"):
+        x = _rand((8, H), dtype, 31)
+        bad = torch.where(keep, x, torch.full_like(x, float("nan")))
+        bad[:, ::3] = torch.where(keep[:, ::3], bad[:, ::3], torch.full_like(bad[:, ::3], float("inf")))
+        r = _rand((8, H), dtype, 32)
+        assert torch.equal(gbn.dropout_forward(bad, 0.5, (21, 22), residual=r),
+                           gbn.dropout_forward(x, 0.5, (21, 22), residual=r))
+        dx, db = gbn.dropout_backward(bad, 0.5, (21, 22), want_dbias=True)
+        dx2, db2 = gbn.dropout_backward(x, 0.5, (21, 22), want_dbias=True)
+        assert torch.equal(dx, dx2) and torch.equal(db, db2)
+        a = gbn.layernorm_dropout_forward(bad, r, 0.5, (21, 22))
+        b = gbn.layernorm_dropout_forward(x, r, 0.5, (21, 22))
+        assert all(torch.equal(a[k], b[k]) for k in a)
+        g, dy = torch.ones(H, device=dev).to(DT[dtype]), _rand((8, H), dtype, 33)
+        a = gbn.layernorm_dropout_backward(dy, bad, r, b["mean"], b["rstd"], g, 0.5, (21, 22))
+        b = gbn.layernorm_dropout_backward(dy, x, r, b["mean"], b["rstd"], g, 0.5, (21, 22))
+        assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.gpu
+def test_aliases_zero_rows_and_repeats(gbn, dev):
+    x = _rand((37, 200), "bf16", 41)
+    r = _rand((37, 200), "bf16", 42)
+    y = gbn.dropout_forward(x, 0.2, (1, 2), residual=r)
+    assert torch.equal(y, gbn.dropout_forward(x, 0.2, (1, 2), residual=r))
+    z = x.clone()
+    assert torch.equal(y, gbn.dropout_forward(z, 0.2, (1, 2), residual=r, y=z))
+    z = r.clone()
+    assert torch.equal(y, gbn.dropout_forward(x, 0.2, (1, 2), residual=z, y=z))
+    e = torch.empty(0, 24, device=dev)
+    assert gbn.dropout_forward(e, 0.2, (1, 2)).numel() == 0
+    dx, db = gbn.dropout_backward(e, 0.2, (1, 2), want_dbias=True)
+    assert dx.numel() == 0 and torch.equal(db, torch.zeros(24, device=dev))
+
+
+@pytest.mark.gpu
+def test_state_on_the_device_and_in_a_graph(gbn, dev):
+    x = _rand((16, 320), "bf16", 51)
+    state = torch.tensor([77, 5], dtype=torch.int64, device=dev)
+    y = gbn.dropout_forward(x, 0.3, state)
+    assert torch.equal(y, gbn.dropout_forward(x, 0.3, (77, 5)))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        gbn.dropout_forward(x, 0.3, state, y=y)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gbn.dropout_forward(x, 0.3, state, y=y)
+    for off in (5, 6):
+        state[1] = off
+        graph.replay()
+        assert torch.equal(y, gbn.dropout_forward(x, 0.3, (77, off)))
+    with pytest.raises(TypeError):
+        gbn.dropout_forward(x, 0.3, state.float())
+    with pytest.raises(TypeError):
+        gbn.dropout_forward(x.half(), 0.3, (1, 2))
+    with pytest.raises(ValueError):
+        gbn.dropout_forward(x.t(), 0.3, (1, 2))
+    with pytest.raises(gbn.GbnError):
+        gbn.dropout_forward(x, 1.2, (1, 2))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gbn, dev):
+    """A tensor of more than 2^32 elements: the last rows draw their own
+    blocks (and addresses)."""
+    R, H = (1 << 20) + 3, 4104
+    x = torch.ones(R, H, dtype=torch.bfloat16, device=dev)
+    gbn.dropout_forward(x, 0.5, (SEED, OFFSET), y=x)
+    for r in (0, R - 1):
+        keep = oracle.dropout_mask(H, 0.5, SEED, OFFSET, start=r * H)
+        assert np.array_equal(_f64(x[r]) != 0, keep), r
+
+
+LN_SHAPES = [(1, 8), (3, 16), (7, 1001), (70, 256), (33, 1600), (5, 20000), (12, 1008), (2, 4),
+             (4, 1), (9, 4096), (40, 72)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,H", LN_SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layernorm(gbn, dev, R, H, dtype):
+    p, rng = 0.15, (SEED, OFFSET)
+    x, r, dy = (_rand((R, H), dtype, s) for s in (61, 62, 63))
+    b, be = _rand((H,), dtype, 64), _rand((H,), dtype, 65)
+    g = (_rand((H,), "f32", 66).abs() + 0.5).to(DT[dtype])
+    m = oracle.dropout_mask(R * H, p, *rng).reshape(R, H)
+    s = oracle.dropout_scale(p)
+    eps = 1e-5 if H > 1 else 0.5
+    out = gbn.layernorm_dropout_forward(x, r, p, rng, g, be, eps, bias=b)
+    ref = oracle.fused_bias_dropout_add_layer_norm_forward(
+        _f64(x), _f64(r), _f64(b), m, s, _f64(g), _f64(be), eps)
+    for k in ("y", "z"):
+        tol.check(out[k], ref[k], f"ln {R}x{H} {dtype} {k}", dtype)
+    tol.check_f32(out["mean"], ref["mean"], "mean")
+    tol.check_f32(out["rstd"], ref["rstd"], "rstd")
+    bw = gbn.layernorm_dropout_backward(dy, x, r, out["mean"], out["rstd"], g, p, rng, bias=b)
+    ref = oracle.fused_bias_dropout_add_layer_norm_backward(
+        _f64(dy), _f64(x), _f64(r), _f64(b), m, s, _f64(out["mean"]), _f64(out["rstd"]), _f64(g))
+    if H == 1:
+        # closed form: a one-element row is its own mean, so xhat and every
+        # gradient through it are 0 (the oracle's differences leave only the
+        # rounding of the saved fp32 mean there)
+        ref.update({k: np.zeros_like(ref[k]) for k in ("dx", "dresidual", "dbias", "dgamma")})
+    for k in ("dx", "dresidual", "dgamma", "dbeta", "dbias"):
+        tol.check(bw[k], ref[k], f"ln bwd {R}x{H} {dtype} {k}", dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,H,mis", [(40, 512, False), (9, 77, False), (6, 64, True)])
+def test_layernorm_variants(gbn, dev, R, H, mis):
+    """No bias, saved z, fp32 residual gradient, an extra gradient at z, no
+    affine, misaligned input; two runs give the same bits; the drawn mask
+    equals the byte mask of the same bits where both exist."""
+    p, rng = 0.3, (5, 6)
+    x, r, dy = (_rand((R, H), "bf16", s, mis) for s in (71, 72, 73))
+    g = _rand((H,), "bf16", 74)
+    extra = _rand((R, H), "f32", 75)
+    m = oracle.dropout_mask(R * H, p, *rng).reshape(R, H)
+    s = oracle.dropout_scale(p)
+    a = gbn.layernorm_dropout_forward(x, r, p, rng, want_z=False)
+    b = gbn.layernorm_dropout_forward(x, r, p, rng)
+    assert a["z"] is None and torch.equal(a["y"], b["y"])
+    tol.check_bf16(b["y"], oracle.fused_bias_dropout_add_layer_norm_forward(
+        _f64(x), _f64(r), None, m, s, None, None, 1e-5)["y"], "no affine")
+    mask = torch.from_numpy(m).to(dev)
+    o = gbn.layernorm_forward(x, None, None, 1e-5, residual=r, mask=mask, dropout_scale=s)
+    tol.check_bf16(b["y"], _f64(o["y"]), "drawn vs stored mask")
+    kw = dict(dz_extra=extra, dres_f32=True)
+    c = gbn.layernorm_dropout_backward(dy, b["z"], None, b["mean"], b["rstd"], g, p, rng,
+                                       saved_z=True, **kw)
+    d = gbn.layernorm_dropout_backward(dy, b["z"], None, b["mean"], b["rstd"], g, p, rng,
+                                       saved_z=True, **kw)
+    assert all(torch.equal(c[k], d[k]) for k in c)
+    ref = oracle.layer_norm_backward_saved_z(_f64(dy), _f64(b["z"]), m, s, _f64(b["mean"]),
+                                             _f64(b["rstd"]), _f64(g), _f64(extra))
+    tol.check_bf16(c["dx"], ref["dx"], "saved z dx")
+    tol.check_bf16(c["dbias"], ref["dbias"], "saved z dbias")
+    # bf16 column and row sums in fp32: a few 2^-24 of terms of size 1
+    np.testing.assert_allclose(_f64(c["dresidual"]), ref["dresidual"], rtol=2e-5, atol=4e-6)
+
+
+@pytest.mark.gpu
+def test_layernorm_long_odd_row(gbn, dev):
+    """Rows past the length whose keep bits fit shared memory."""
+    R, H = 1, (1 << 18) + 5
+    x, r, dy = (_rand((R, H), "f32", s) for s in (81, 82, 83))
+    g = torch.ones(H, device=dev)
+    m = oracle.dropout_mask(R * H, 0.2, 1, 2).reshape(R, H)
+    s = oracle.dropout_scale(0.2)
+    out = gbn.layernorm_dropout_forward(x, r, 0.2, (1, 2))
+    ref = oracle.fused_bias_dropout_add_layer_norm_forward(_f64(x), _f64(r), None, m, s, None,
+                                                           None, 1e-5)
+    tol.check_f32(out["y"], ref["y"], "long y")
+    bw = gbn.layernorm_dropout_backward(dy, x, r, out["mean"], out["rstd"], g, 0.2, (1, 2))
+    ref = oracle.fused_bias_dropout_add_layer_norm_backward(
+        _f64(dy), _f64(x), _f64(r), None, m, s, _f64(out["mean"]), _f64(out["rstd"]), _f64(g))
+    tol.check_f32(bw["dx"], ref["dx"], "long dx")
