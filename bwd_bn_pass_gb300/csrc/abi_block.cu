@@ -1,7 +1,9 @@
 // extern "C" entry points of the backbone-block operators (declared in
-// include/gbnorm.h): dropout with a counter-based mask, alone and inside
-// LayerNorm.  As in abi.cu, arguments are validated before CUDA is touched,
+// include/gbnorm.h): GroupNorm with an activation (channels last), and dropout
+// with a counter-based mask, alone and inside LayerNorm.  As in abi.cu, arguments are validated before CUDA is touched,
 // and every call only launches on the caller's stream.
+#include <cmath>
+
 #include "gbn_internal.h"
 #include "philox.cuh"
 
@@ -16,9 +18,77 @@ int rng_check(double p, const uint64_t* state) {
   return GBN_OK;
 }
 
+int gn_check(int dtype, int64_t N, int64_t S, int64_t C, int64_t G, int act, float slope) {
+  if (dtype != GBN_F32 && dtype != GBN_BF16) return GBN_EDTYPE;
+  if (N < 0 || S < 0 || C < 0 || C > (1 << 30) || N > INT32_MAX) return GBN_EINVAL;
+  if (G < 1 || G > INT32_MAX || C % G != 0) return GBN_EINVAL;
+  int64_t m, n;
+  if (!mul_ok(N, S, &m) || !mul_ok(m, C, &n) || n > (INT64_MAX >> 3)) return GBN_EINVAL;
+  if (N > 0 && C > 0 && S == 0) return GBN_EINVAL;  // the mean over nothing is undefined
+  if (act < GBN_ACT_NONE || act > GBN_ACT_SILU) return GBN_EINVAL;
+  if (act == GBN_ACT_LEAKY_RELU && !std::isfinite(slope)) return GBN_EINVAL;
+  return GBN_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+// ------------------------------------------- GroupNorm, channels last --
+
+size_t gbn_gn_nhwc_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int device) {
+  if (gn_check(GBN_F32, N, S, C, G, GBN_ACT_NONE, 0.f) != GBN_OK) return 0;
+  if (N == 0 || C == 0) return 256;
+  const DevInfo* dev = device_info(device);
+  if (!dev) return 0;
+  return gn_ws_bound(N, S, C, G, *dev);
+}
+
+int gbn_gn_nhwc_forward_train(const void* x, int dtype, int64_t N, int64_t S, int64_t C,
+                              int64_t G, const float* gamma, const float* beta, float eps,
+                              int act, float slope, void* y, float* stats, void* ws,
+                              size_t ws_bytes, void* stream) {
+  const int rc = gn_check(dtype, N, S, C, G, act, slope);
+  if (rc != GBN_OK) return rc;
+  if (!(eps >= 0.f)) return GBN_EINVAL;
+  if (N == 0 || C == 0) return GBN_OK;
+  if (x == nullptr || y == nullptr || stats == nullptr || ws == nullptr) return GBN_EINVAL;
+  if (!aligned(ws, 16)) return GBN_EALIGN;
+  const DevInfo* dev = device_info(-1);
+  if (!dev) return GBN_ECUDA;
+  const void* ptrs[2] = {x, y};
+  GnPlan p;
+  if (!gn_plan(N, S, C, G, bn_vec_width(dtype, C, ptrs, 2), false, *dev, &p)) return GBN_EINVAL;
+  if (ws_bytes < p.ws_bytes) return GBN_EWORKSPACE;
+  return to_status(gn_forward(p, dtype, x, gamma, beta, eps, act, slope, y, stats, ws,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+int gbn_gn_nhwc_backward(const void* x, const void* dy, int dtype, int64_t N, int64_t S,
+                         int64_t C, int64_t G, const float* stats, const float* gamma,
+                         const float* beta, int act, float slope, void* dx, float* dgamma,
+                         float* dbeta, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = gn_check(dtype, N, S, C, G, act, slope);
+  if (rc != GBN_OK) return rc;
+  if (C == 0 || (N == 0 && dgamma == nullptr && dbeta == nullptr)) return GBN_OK;
+  if (N > 0 && (x == nullptr || dy == nullptr || dx == nullptr || stats == nullptr ||
+                ws == nullptr))
+    return GBN_EINVAL;
+  if (!aligned(ws, 16)) return GBN_EALIGN;
+  const DevInfo* dev = device_info(-1);
+  if (!dev) return GBN_ECUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (N == 0) {  // the parameter gradients are sums of nothing
+    void* outs[3] = {dgamma, dbeta, nullptr};
+    return to_status(colsum_launch(nullptr, 2, 2, 0, C, GBN_F32, outs, st, false));
+  }
+  const void* ptrs[3] = {x, dy, dx};
+  GnPlan p;
+  if (!gn_plan(N, S, C, G, bn_vec_width(dtype, C, ptrs, 3), true, *dev, &p)) return GBN_EINVAL;
+  if (ws_bytes < p.ws_bytes) return GBN_EWORKSPACE;
+  return to_status(gn_backward(p, dtype, x, dy, stats, gamma, beta, act, slope, dx, dgamma, dbeta,
+                               ws, st));
+}
 
 // -------------------------------------------------------------- dropout --
 

@@ -301,6 +301,32 @@ cudaError_t row_kernels_configure(int smem_optin);
 // GBN_DEV_WAIT_TIMEOUT in *status.
 cudaError_t selftest_bounded_wait(int* status, uint64_t limit_ns, cudaStream_t st);
 
+// -------------------------------------------- GroupNorm, channels last --
+
+struct GnPlan {
+  int64_t N = 0, S = 0, C = 0, G = 0;  // samples, rows per sample, channels, groups
+  int vec = 1;              // channels per vector (divides C)
+  int TX = 1, TY = 1;       // block shape: vectors x rows
+  int tiles = 1;            // channel tiles of TX vectors
+  int slices = 1;           // row slices per sample
+  int threads = 32;         // block size
+  int tile_groups = 1;      // groups a tile can touch, at most
+  int64_t blocks = 0;       // N * slices * tiles
+  size_t gpart_bytes = 0;   // group partials; the channel partials follow
+  size_t ws_bytes = 0;
+};
+bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, bool backward,
+             const DevInfo& dev, GnPlan* p);
+// Workspace for any vector width and direction.
+size_t gn_ws_bound(int64_t N, int64_t S, int64_t C, int64_t G, const DevInfo& dev);
+cudaError_t gn_forward(const GnPlan& p, int dtype, const void* x, const float* gamma,
+                       const float* beta, float eps, int act, float slope, void* y, float* stats,
+                       void* ws, cudaStream_t st);
+cudaError_t gn_backward(const GnPlan& p, int dtype, const void* x, const void* dy,
+                        const float* stats, const float* gamma, const float* beta, int act,
+                        float slope, void* dx, float* dgamma, float* dbeta, void* ws,
+                        cudaStream_t st);
+
 // ------------------------------------------ dropout, mask never stored --
 
 constexpr int kDBlocksPerSm = 4;  // 256-thread blocks per SM the grid fills

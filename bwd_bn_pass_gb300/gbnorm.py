@@ -29,6 +29,9 @@ GBN_ACT_LEAKY_RELU = 2
 _ACTS = {None: GBN_ACT_NONE, "none": GBN_ACT_NONE, "relu": GBN_ACT_RELU,
          "leaky_relu": GBN_ACT_LEAKY_RELU}
 
+GBN_ACT_SILU = 3
+_GN_ACTS = {**_ACTS, "silu": GBN_ACT_SILU}
+
 _DTYPE_CODE = {torch.float32: GBN_F32, torch.bfloat16: GBN_BF16}
 
 _lib = None
@@ -101,6 +104,11 @@ _SIGNATURES = {
     "gbn_rmsnorm_forward": (_INT, [_P, _P, _INT, _I64, _I64, _F, _P, _P, _P]),
     "gbn_layernorm_forward": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P, _F, _P, _P, _F, _P, _P,
                                      _P, _P, _P]),
+    "gbn_gn_nhwc_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _INT]),
+    "gbn_gn_nhwc_forward_train": (_INT, [_P, _INT, _I64, _I64, _I64, _I64, _P, _P, _F, _INT, _F,
+                                         _P, _P, _P, _SZ, _P]),
+    "gbn_gn_nhwc_backward": (_INT, [_P, _P, _INT, _I64, _I64, _I64, _I64, _P, _P, _P, _INT, _F,
+                                    _P, _P, _P, _P, _SZ, _P]),
     "gbn_dropout_forward": (_INT, [_P, _INT, _I64, _I64, _P, _P, _D, _U64, _U64, _P, _P, _P]),
     "gbn_dropout_workspace_bytes": (_SZ, [_I64, _I64, _INT, _INT]),
     "gbn_dropout_backward": (_INT, [_P, _INT, _I64, _I64, _D, _U64, _U64, _P, _P, _P, _P, _SZ,
@@ -682,6 +690,90 @@ def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, *, residual=None, bias
             _ptr(mean), _ptr(rstd), _stream(x.device))
     _check("gbn_layernorm_forward", st)
     return {"y": y, "z": z, "mean": mean, "rstd": rstd}
+
+
+# --------------------------------------------- GroupNorm, channels last --
+
+def _gn_dims(x, groups):
+    if _cuda(x, "x").dim() < 2:
+        raise ValueError("channels-last GroupNorm wants a contiguous [N, ..., C] tensor")
+    N, C = x.shape[0], x.shape[-1]
+    if groups < 1 or C % groups:
+        raise ValueError(f"{groups} groups do not divide {C} channels")
+    return N, math.prod(x.shape[1:-1]), C
+
+
+def _gn_act(act):
+    if act not in _GN_ACTS:
+        raise ValueError(f"act must be one of {sorted(k for k in _GN_ACTS if k)} or None")
+    return _GN_ACTS[act]
+
+
+def gn_nhwc_workspace(x, groups):
+    N, S, C = _gn_dims(x, groups)
+    with torch.cuda.device(x.device):
+        n = lib().gbn_gn_nhwc_workspace_bytes(N, S, C, groups, -1)
+    if n == 0:
+        raise ValueError(f"bad channels-last GroupNorm shape {tuple(x.shape)}")
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def gn_nhwc_forward_train(x, groups, gamma=None, beta=None, eps=1e-5, *, act=None, slope=0.01,
+                          y=None, stats=None, ws=None):
+    """Channels-last GroupNorm training forward followed by ``act`` ("relu",
+    "leaky_relu" with negative slope ``slope``, "silu" or None): x is a
+    contiguous [N, ..., C] tensor, the groups are runs of C / groups adjacent
+    channels.  Returns (y, stats) with stats fp32 [3, N, groups] = (mean, rstd,
+    the mean's remainder)."""
+    code = _gn_act(act)
+    N, S, C = _gn_dims(x, groups)
+    _fp32_vec(gamma, "gamma", C)
+    _fp32_vec(beta, "beta", C)
+    y = torch.empty_like(x) if y is None else _like(y, x, "y")
+    if stats is None:
+        stats = torch.empty(3, N, groups, dtype=torch.float32, device=x.device)
+    else:
+        _fp32_vec(stats, "stats", 3 * N * groups)
+    ws = gn_nhwc_workspace(x, groups) if ws is None else _cuda(ws, "ws")
+    _same_device(x, ("y", y), ("stats", stats), ("ws", ws), ("gamma", gamma), ("beta", beta))
+    with torch.cuda.device(x.device):
+        st = lib().gbn_gn_nhwc_forward_train(
+            _ptr(x), _code(x.dtype), N, S, C, groups, _ptr(gamma), _ptr(beta), float(eps), code,
+            float(slope), _ptr(y), _ptr(stats), _ptr(ws), ws.numel() * ws.element_size(),
+            _stream(x.device))
+    _check("gbn_gn_nhwc_forward_train", st)
+    return y, stats
+
+
+def gn_nhwc_backward(x, dy, stats, gamma=None, beta=None, *, act=None, slope=0.01, dx=None,
+                     dgamma=None, dbeta=None, ws=None):
+    """Backward of ``gn_nhwc_forward_train`` from its ``stats``, with the same
+    gamma, beta, act and slope.  Returns (dx, dgamma, dbeta), the last two
+    fp32 [C]."""
+    code = _gn_act(act)
+    if _cuda(stats, "stats").dim() != 3 or stats.shape[0] != 3:
+        raise ValueError("stats must be the forward's [3, N, groups] tensor")
+    groups = stats.shape[2]
+    N, S, C = _gn_dims(x, groups)
+    _fp32_vec(stats, "stats", 3 * N * groups)
+    _like(dy, x, "dy")
+    dx = torch.empty_like(x) if dx is None else _like(dx, x, "dx")
+    if dgamma is None:
+        dgamma = torch.empty(C, dtype=torch.float32, device=x.device)
+    if dbeta is None:
+        dbeta = torch.empty(C, dtype=torch.float32, device=x.device)
+    for name, t in (("gamma", gamma), ("beta", beta), ("dgamma", dgamma), ("dbeta", dbeta)):
+        _fp32_vec(t, name, C)
+    ws = gn_nhwc_workspace(x, groups) if ws is None else _cuda(ws, "ws")
+    _same_device(x, ("dy", dy), ("stats", stats), ("gamma", gamma), ("beta", beta), ("dx", dx),
+                 ("dgamma", dgamma), ("dbeta", dbeta), ("ws", ws))
+    with torch.cuda.device(x.device):
+        st = lib().gbn_gn_nhwc_backward(
+            _ptr(x), _ptr(dy), _code(x.dtype), N, S, C, groups, _ptr(stats), _ptr(gamma),
+            _ptr(beta), code, float(slope), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
+            ws.numel() * ws.element_size(), _stream(x.device))
+    _check("gbn_gn_nhwc_backward", st)
+    return dx, dgamma, dbeta
 
 
 # ------------------------------------------- dropout, mask never stored --

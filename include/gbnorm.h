@@ -476,6 +476,45 @@ GBN_API int gbn_layernorm_forward(const void* x_or_input, int dtype, int64_t R, 
                                   void* z, float* mean, float* rstd, void* stream);
 
 /* =========================================================================
+ * GroupNorm, training mode, channels last, with an activation.
+ *
+ * x, y, dy, dx: [N, S, C] row-major in `dtype` (a channels-last [N, H, W, C]
+ * tensor with S = H*W); G groups of C/G adjacent channels (G divides C).  For
+ * sample n and group g, over its S*C/G elements (biased variance):
+ *   mean, rstd = 1/sqrt(var + eps),  xhat = (x - mean)*rstd,
+ *   pre = xhat*gamma_c + beta_c,     y = act(pre)
+ * and, with e = dy*act'(pre) (pre is recomputed, nothing of it is stored),
+ *   dbeta_c = sum_{n,s} e,  dgamma_c = sum_{n,s} e*xhat,
+ *   dx = rstd*(gamma_c*e - mean_g(gamma*e) - xhat*mean_g(gamma*e*xhat)).
+ * act: GBN_ACT_NONE, _RELU, _LEAKY_RELU (negative slope `slope`, finite) or
+ * GBN_ACT_SILU (pre*sigmoid(pre)); SILU is GroupNorm's alone.
+ * gamma, beta: fp32 [C] or NULL (ones / zeros).
+ * stats: fp32 [3, N, G] = (mean rounded to fp32, rstd, mean's remainder), which
+ * the forward writes and the backward takes.
+ * S = 0 with N > 0 is GBN_EINVAL (a mean over nothing); N = 0 is GBN_OK.
+ * ws: 16-byte aligned, at least gbn_gn_nhwc_workspace_bytes bytes.
+ * ======================================================================= */
+#define GBN_ACT_SILU 3
+
+/* Workspace bytes of either direction (-1: current device); 0 on a bad shape
+ * or a CUDA error.                                                          */
+GBN_API size_t gbn_gn_nhwc_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G,
+                                           int device);
+
+/* Training forward: writes y and stats.  y may alias x.                     */
+GBN_API int gbn_gn_nhwc_forward_train(const void* x, int dtype, int64_t N, int64_t S, int64_t C,
+                                      int64_t G, const float* gamma, const float* beta, float eps,
+                                      int act, float slope, void* y, float* stats, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* Backward from the forward's stats, gamma, beta, act and slope: writes dx
+ * and, unless NULL, dgamma and dbeta (fp32 [C]).  dx may alias dy or x.     */
+GBN_API int gbn_gn_nhwc_backward(const void* x, const void* dy, int dtype, int64_t N, int64_t S,
+                                 int64_t C, int64_t G, const float* stats, const float* gamma,
+                                 const float* beta, int act, float slope, void* dx, float* dgamma,
+                                 float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* =========================================================================
  * Dropout from a counter-based generator: the mask is drawn where it is used
  * and never stored.
  *

@@ -40,6 +40,7 @@ from .layernorm import (
     fused_bias_dropout_add_layer_norm_backward,
     layer_norm_backward_saved_z,
 )
+from .groupnorm import group_norm_act, group_norm_act_gate, group_norm_forward, group_norm_backward
 from .dropout import (
     philox4x32_10,
     dropout_threshold,
@@ -69,6 +70,10 @@ __all__ = [
     "layer_norm_backward",
     "fused_bias_dropout_add_layer_norm_backward",
     "layer_norm_backward_saved_z",
+    "group_norm_act",
+    "group_norm_act_gate",
+    "group_norm_forward",
+    "group_norm_backward",
     "philox4x32_10",
     "dropout_threshold",
     "dropout_scale",

@@ -1,0 +1,300 @@
+"""GroupNorm with an activation, channels last: the oracle against autograd
+and differences, refusals, and the CUDA path against the oracle.
+
+Tolerances.  y and dx: those of every parity test (tests/tolerances.py).
+dgamma and dbeta are fp32 sums of M terms t_i that are themselves rounded fp32
+values: each term is off by a few half steps (its factors (x - mean), the gate
+and their products: at most 8 * 2^-24 relative to |dy| * (1 + |xhat|)), and the
+sums are carried with their errors per few rows, so the bound is
+16 * 2^-24 * sum_i |t_i| + 1e-6."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+from . import tolerances as tol
+
+DEV = "cuda:0"
+OK, EINVAL, EDTYPE, EALIGN, EWORKSPACE = 0, -1, -2, -3, -4
+P = ctypes.c_void_p
+A16, A4 = P(0x10000), P(0x10004)
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+# ------------------------------------------------------------- the oracle
+
+@pytest.mark.parametrize("act", [None, "relu", "leaky_relu", "silu"])
+def test_oracle_matches_autograd(act):
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(2, 5, 3, 12, generator=g, dtype=torch.float64, requires_grad=True)
+    gm = torch.randn(12, generator=g, dtype=torch.float64, requires_grad=True)
+    be = torch.randn(12, generator=g, dtype=torch.float64, requires_grad=True)
+    dy = torch.randn(2, 5, 3, 12, generator=g, dtype=torch.float64)
+    y = torch.nn.functional.group_norm(x.permute(0, 3, 1, 2), 4, gm, be, 1e-5).permute(0, 2, 3, 1)
+    f = {None: lambda v: v, "relu": torch.relu, "silu": torch.nn.functional.silu,
+         "leaky_relu": lambda v: torch.nn.functional.leaky_relu(v, 0.2)}[act]
+    y = f(y)
+    y.backward(dy)
+    n = [t.detach().numpy() for t in (x, gm, be, dy)]
+    fw = oracle.group_norm_forward(n[0], 4, n[1], n[2], 1e-5, act, 0.2)
+    bw = oracle.group_norm_backward(n[0], n[3], 4, fw["mean"], fw["rstd"], n[1], n[2], act, 0.2)
+    np.testing.assert_allclose(fw["y"], y.detach().numpy(), rtol=1e-12, atol=1e-12)
+    for k, t in (("dx", x), ("dgamma", gm), ("dbeta", be)):
+        np.testing.assert_allclose(bw[k], t.grad.numpy(), rtol=1e-10, atol=1e-11)
+
+
+def test_oracle_matches_differences():
+    g = np.random.default_rng(2)
+    x, dy = g.normal(size=(1, 3, 4)), g.normal(size=(1, 3, 4))
+    gm, be = g.normal(size=4), g.normal(size=4)
+
+    def loss(xx):
+        return (oracle.group_norm_forward(xx, 2, gm, be, 1e-5, "silu")["y"] * dy).sum()
+
+    fw = oracle.group_norm_forward(x, 2, gm, be, 1e-5, "silu")
+    bw = oracle.group_norm_backward(x, dy, 2, fw["mean"], fw["rstd"], gm, be, "silu")
+    for i in np.ndindex(x.shape):
+        e = np.zeros_like(x)
+        e[i] = 1e-6
+        assert abs((loss(x + e) - loss(x - e)) / 2e-6 - bw["dx"][i]) < 1e-7
+
+
+# --------------------------------------------------------------- refusals
+
+def test_argument_errors(gbn):
+    L = gbn.lib()
+
+    def fwd(x=A16, dtype=0, N=2, S=3, C=8, G=2, eps=1e-5, act=0, slope=0.0, y=A16, st=A16, ws=A16,
+            n=1 << 20):
+        return L.gbn_gn_nhwc_forward_train(x, dtype, N, S, C, G, None, None, eps, act, slope, y, st,
+                                           ws, n, None)
+
+    def bwd(x=A16, dy=A16, dtype=0, N=2, S=3, C=8, G=2, st=A16, act=0, slope=0.0, dx=A16, ws=A16,
+            n=1 << 20):
+        return L.gbn_gn_nhwc_backward(x, dy, dtype, N, S, C, G, st, None, None, act, slope, dx,
+                                      None, None, ws, n, None)
+
+    for f in (fwd, bwd):
+        assert f(dtype=2) == EDTYPE
+        for kw in ({"x": None}, {"st": None}, {"ws": None}, {"N": -1}, {"S": -1}, {"C": -8},
+                   {"G": 0}, {"G": 3}, {"G": 16}, {"S": 0}, {"act": 4}, {"act": -1},
+                   {"act": 2, "slope": float("nan")}, {"N": 1 << 30, "S": 1 << 40}):
+            assert f(**kw) == EINVAL, kw
+        assert f(ws=A4) == EALIGN
+        assert f(N=0) == OK
+        assert f(C=0, G=1) == OK
+    assert fwd(y=None) == EINVAL
+    assert fwd(eps=-1.0) == EINVAL
+    assert fwd(eps=float("nan")) == EINVAL
+    assert bwd(dy=None) == EINVAL
+    assert bwd(dx=None) == EINVAL
+    assert L.gbn_gn_nhwc_workspace_bytes(2, 3, 8, 3, -1) == 0
+
+
+def test_binding_refusals(gbn):
+    x = torch.zeros(2, 3, 8)
+    with pytest.raises(ValueError):
+        gbn.gn_nhwc_forward_train(x, 2)
+    with pytest.raises(ValueError):
+        gbn.gn_nhwc_forward_train(x, 2, act="gelu")
+
+
+# ----------------------------------------------------------------- the GPU
+
+@pytest.fixture
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return DEV
+
+
+def _f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def _inputs(shape, dtype, seed, spread=2.0, mis=False):
+    g = torch.Generator().manual_seed(seed)
+    C = shape[-1]
+    mu = (torch.rand(C, generator=g) - 0.5) * 2 * spread
+    t = mu + torch.randn(shape, generator=g) * (0.5 + torch.rand(C, generator=g))
+    out = []
+    for v in (t, torch.randn(shape, generator=g)):
+        v = v.to(DT[dtype])
+        if mis:
+            big = torch.zeros(v.numel() + 1, dtype=v.dtype, device=DEV)
+            big[1:] = v.reshape(-1).to(DEV)
+            out.append(big[1:].view(shape))
+        else:
+            out.append(v.to(DEV))
+    gamma = (0.5 + torch.rand(C, generator=g)).to(DEV)
+    beta = (0.1 * torch.randn(C, generator=g)).to(DEV)
+    return out[0], out[1], gamma, beta
+
+
+def _check(gbn, x, dy, gamma, beta, G, dtype, act, what, slope=0.01):
+    y, stats = gbn.gn_nhwc_forward_train(x, G, gamma, beta, 1e-5, act=act, slope=slope)
+    ref = oracle.group_norm_forward(_f64(x), G, _f64(gamma), _f64(beta), 1e-5, act, slope)
+    tol.check(y, ref["y"], f"{what} y", dtype)
+    tol.check_f32(stats[0], ref["mean"], f"{what} mean")
+    tol.check_f32(stats[1], ref["rstd"], f"{what} rstd")
+    dx, dg, db = gbn.gn_nhwc_backward(x, dy, stats, gamma, beta, act=act, slope=slope)
+    s64 = _f64(stats)
+    bw = oracle.group_norm_backward(_f64(x), _f64(dy), G, s64[0] + s64[2], s64[1], _f64(gamma),
+                                    _f64(beta), act, slope)
+    tol.check(dx, bw["dx"], f"{what} dx", dtype)
+    cen = (_f64(x).reshape(x.shape[0], -1, G, x.shape[-1] // G)
+           - (s64[0] + s64[2])[:, None, :, None]) * s64[1][:, None, :, None]
+    axes = tuple(range(x.dim() - 1))
+    xh = np.abs(cen).reshape(x.shape)
+    for k, got, w in (("dgamma", dg, xh), ("dbeta", db, 1.0)):
+        bound = 16 * 2.0 ** -24 * (np.abs(_f64(dy)) * (1 + xh) * w).sum(axis=axes) + 1e-6
+        err = np.abs(_f64(got) - bw[k])
+        assert np.all(err <= bound), f"{what} {k}: {np.max(err / bound)} of the bound"
+    return y, stats, dx, dg, db
+
+
+SHAPES = [  # N, spatial..., C, G
+    ((1, 8, 8, 64), 32), ((2, 7, 5, 320), 32), ((3, 41, 10, 37), 1), ((1, 1, 2), 1),
+    ((2, 3, 3, 1), 1), ((4, 1, 1, 48), 8), ((1, 30, 6, 4104), 3), ((2, 9, 2080), 4),
+    ((1, 300, 12), 12), ((5, 17, 8), 2), ((1, 1000, 4), 1), ((2, 50, 6), 3), ((70, 2, 24), 4),
+    ((1, 5, 2049), 1), ((2, 64, 16), 16),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,G", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_parity(gbn, dev, shape, G, dtype, act):
+    x, dy, gamma, beta = _inputs(shape, dtype, sum(shape) + G)
+    _check(gbn, x, dy, gamma, beta, G, dtype, act, f"gn {shape} {G} {dtype} {act}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["relu", "leaky_relu"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gated_activations(gbn, dev, dtype, act):
+    """pre values next to 0 are kept away from the gate: their side is the
+    same in 32 and in 64 bits."""
+    x, dy, gamma, beta = _inputs((2, 13, 24), dtype, 5)
+    pre = oracle.group_norm_forward(_f64(x), 4, _f64(gamma), _f64(beta), 1e-5)["pre"]
+    assert np.abs(pre).min() > 1e-5
+    _check(gbn, x, dy, gamma, beta, 4, dtype, act, f"gn {act} {dtype}", slope=0.2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_shapes_and_options(gbn, dev, dtype):
+    x, dy, gamma, beta = _inputs((3, 11, 40), dtype, 7, mis=True)  # not 16-byte aligned
+    _check(gbn, x, dy, gamma, beta, 4, dtype, "silu", "misaligned")
+    _check(gbn, x, dy, None, None, 4, dtype, "silu", "no affine")
+    x, dy, gamma, beta = _inputs((2, 64, 64, 320), dtype, 8)       # many slices
+    a = _check(gbn, x, dy, gamma, beta, 32, dtype, "silu", "many slices")
+    b = _check(gbn, x, dy, gamma, beta, 32, dtype, "silu", "many slices")
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    z = x.clone()
+    assert torch.equal(gbn.gn_nhwc_forward_train(z, 32, gamma, beta, act="silu", y=z)[0], a[0])
+    z = dy.clone()
+    assert torch.equal(gbn.gn_nhwc_backward(x, z, a[1], gamma, beta, act="silu", dx=z)[0], a[2])
+    z = x.clone()
+    assert torch.equal(gbn.gn_nhwc_backward(z, dy, a[1], gamma, beta, act="silu", dx=z)[0], a[2])
+
+
+@pytest.mark.gpu
+def test_large_offset_and_an_outlier_first_row(gbn, dev):
+    """A common offset of 1000 with unit spread, and a first row far from all
+    others (a padded border): neither costs the variance anything."""
+    x, dy, gamma, beta = _inputs((2, 40, 64), "f32", 9, spread=0.5)
+    _check(gbn, x + 1000.0, dy, gamma, beta, 8, "f32", None, "offset")
+    z = x + 1000.0
+    z[:, 0] = 0.0
+    y, stats = gbn.gn_nhwc_forward_train(z, 8, gamma, beta)
+    ref = oracle.group_norm_forward(_f64(z), 8, _f64(gamma), _f64(beta), 1e-5)
+    tol.check_f32(y, ref["y"], "border y")
+    tol.check_f32(stats[1], ref["rstd"], "border rstd")
+    big = torch.full((1, 5000, 16), 1000.0, device=dev)
+    big[:, 1:] += torch.randn(1, 4999, 16, device=dev, generator=torch.Generator(dev).manual_seed(3))
+    big[:, 0] = 0.0
+    y, stats = gbn.gn_nhwc_forward_train(big, 16)
+    ref = oracle.group_norm_forward(_f64(big), 16)
+    tol.check_f32(stats[1], ref["rstd"], "outlier rstd")
+
+
+@pytest.mark.gpu
+def test_constant_groups_and_empty_batches(gbn, dev):
+    x = torch.full((2, 9, 8), 3.25, device=dev)
+    y, stats = gbn.gn_nhwc_forward_train(x, 2, act="silu")
+    assert torch.equal(y, torch.zeros_like(y))
+    assert torch.equal(stats[0], torch.full((2, 2), 3.25, device=dev))
+    e = torch.empty(0, 4, 8, device=dev)
+    y, stats = gbn.gn_nhwc_forward_train(e, 2)
+    dx, dg, db = gbn.gn_nhwc_backward(e, e, stats)
+    assert dx.numel() == 0 and not dg.any() and not db.any()
+    with pytest.raises(ValueError):
+        gbn.gn_nhwc_forward_train(x, 3)
+    with pytest.raises(ValueError):
+        gbn.gn_nhwc_forward_train(x.transpose(1, 2), 1)
+    with pytest.raises(TypeError):
+        gbn.gn_nhwc_forward_train(x.half(), 2)
+    with pytest.raises(TypeError):
+        gbn.gn_nhwc_forward_train(x, 2, gamma=torch.ones(8, device=dev, dtype=torch.bfloat16))
+
+
+@pytest.mark.gpu
+def test_nan_stays_in_its_group(gbn, dev):
+    x, dy, gamma, beta = _inputs((2, 12, 16), "f32", 11)
+    ok, _ = gbn.gn_nhwc_forward_train(x, 4, gamma, beta, act="silu")
+    x[1, 3, 5] = float("nan")
+    y, _ = gbn.gn_nhwc_forward_train(x, 4, gamma, beta, act="silu")
+    assert y[1, :, 4:8].isnan().all()
+    assert torch.equal(y[0], ok[0]) and torch.equal(y[1, :, 8:], ok[1, :, 8:])
+
+
+@pytest.mark.gpu
+def test_other_stream_and_graph(gbn, dev):
+    x, dy, gamma, beta = _inputs((2, 100, 64), "bf16", 13)
+    y, stats = gbn.gn_nhwc_forward_train(x, 8, gamma, beta, act="silu")
+    grads = gbn.gn_nhwc_backward(x, dy, stats, gamma, beta, act="silu")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y2, st2 = gbn.gn_nhwc_forward_train(x, 8, gamma, beta, act="silu")
+        g2 = gbn.gn_nhwc_backward(x, dy, st2, gamma, beta, act="silu")
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, y2) and all(torch.equal(p, q) for p, q in zip(grads, g2))
+    outs = [torch.zeros_like(t) for t in (y, stats, *grads)]
+    wsp = gbn.gn_nhwc_workspace(x, 8)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gbn.gn_nhwc_forward_train(x, 8, gamma, beta, act="silu", y=outs[0], stats=outs[1], ws=wsp)
+        gbn.gn_nhwc_backward(x, dy, outs[1], gamma, beta, act="silu", dx=outs[2], dgamma=outs[3],
+                             dbeta=outs[4], ws=wsp)
+    for _ in range(3):
+        for t in outs:
+            t.zero_()
+        wsp.fill_(0xFF)
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(outs, (y, stats, *grads)))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gbn, dev):
+    """More than 2^32 elements: the last sample equals the same sample alone."""
+    N, S, C = 3, (1 << 21) + 5, 704
+    x = torch.empty(N, S, C, dtype=torch.bfloat16, device=dev)
+    x.normal_(generator=torch.Generator(dev).manual_seed(17))
+    y, stats = gbn.gn_nhwc_forward_train(x, 32, act="silu")
+    one = x[N - 1:].clone()
+    xd = one[0].double().view(S, 32, C // 32)
+    m = xd.mean(dim=(0, 2))
+    r = (xd.var(dim=(0, 2), unbiased=False) + 1e-5).rsqrt()
+    del xd
+    tol.check_f32(stats[0, N - 1], m.cpu(), "last mean")
+    tol.check_f32(stats[1, N - 1], r.cpu(), "last rstd")
+    rows = one[0, -3:].double().view(3, 32, C // 32)
+    pre = ((rows - m.view(1, 32, 1)) * r.view(1, 32, 1)).view(3, C)
+    tol.check_bf16(y[N - 1, -3:], _f64(pre * torch.sigmoid(pre)), "last rows")
