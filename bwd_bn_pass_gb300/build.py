@@ -23,7 +23,7 @@ LIB_NAME = "libgbnorm.so"
 SOURCES = ["abi.cu", "bn_kernels.cu", "rms_kernels.cu", "ln_kernels.cu",
            "row_common.cu", "noalloc.cu", "bn_fused.cu", "bn_small.cu", "fwd_kernels.cu",
            "bn_nhwc.cu", "selftest.cu", "abi_block.cu", "dropout.cu",
-           "gn.cu"]
+           "gn.cu", "rope.cu"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

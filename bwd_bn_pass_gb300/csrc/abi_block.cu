@@ -1,6 +1,7 @@
 // extern "C" entry points of the backbone-block operators (declared in
-// include/gbnorm.h): GroupNorm with an activation (channels last), and dropout
-// with a counter-based mask, alone and inside LayerNorm.  As in abi.cu, arguments are validated before CUDA is touched,
+// include/gbnorm.h): GroupNorm with an activation (channels last), RMSNorm of
+// attention heads with rotary positions, and dropout with a counter-based
+// mask, alone and inside LayerNorm.  As in abi.cu, arguments are validated before CUDA is touched,
 // and every call only launches on the caller's stream.
 #include <cmath>
 
@@ -30,9 +31,150 @@ int gn_check(int dtype, int64_t N, int64_t S, int64_t C, int64_t G, int act, flo
   return GBN_OK;
 }
 
+int rope_check(int dtype, int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, int layout,
+               float scale) {
+  if (dtype != GBN_F32 && dtype != GBN_BF16) return GBN_EDTYPE;
+  if (T < 0 || H < 0 || H > 65535 || D < 1 || D > kRopeMaxD) return GBN_EINVAL;
+  if (HQ < 0 || HQ > H || (H > 0 && HQ < 1)) return GBN_EINVAL;
+  if (rot < 0 || rot > D || rot % 2 != 0) return GBN_EINVAL;
+  if (layout != GBN_ROPE_HALF && layout != GBN_ROPE_INTERLEAVED) return GBN_EINVAL;
+  if (!std::isfinite(scale)) return GBN_EINVAL;
+  int64_t n;
+  if (!mul_ok(T, H * D, &n) || n > (INT64_MAX >> 3) || T > ((int64_t)1 << 36)) return GBN_EINVAL;
+  return GBN_OK;
+}
+
+// Strides of at least a row, so that no two outputs overlap (the last heads
+// and tokens included); zero strides are not rows.
+bool rope_strides(int64_t T, int64_t H, int64_t D, int64_t t, int64_t h) {
+  if (t < 0 || h < 0) return false;
+  if (H > 1 && h < D) return false;
+  if (T > 1 && t < D) return false;
+  int64_t a, b;
+  return mul_ok(T, t, &a) && mul_ok(H, h, &b) && a < (INT64_MAX >> 4) && b < (INT64_MAX >> 4);
+}
+
+// Widest vector (elements, at most 8) that a base and its strides allow.
+int rope_vec(const void* p, int64_t T, int64_t H, int64_t t, int64_t h, int64_t esize) {
+  int v = (int)(16 / esize);
+  while (v > 1 && (!aligned(p, (uintptr_t)(v * esize)) || (T > 1 && t % v != 0) ||
+                   (H > 1 && h % v != 0)))
+    v /= 2;
+  return v;
+}
+
+int rope_call(RopePtrs q, int dir, int dtype, int64_t T, int64_t H, int64_t HQ, int64_t D,
+              int64_t rot, int layout, float scale, float eps, size_t ws_bytes, void* stream) {
+  const DevInfo* dev = device_info(-1);
+  if (!dev) return GBN_ECUDA;
+  const int64_t es = dtype == GBN_F32 ? 4 : 2;
+  int v = rope_vec(q.out, T, H, q.yt, q.yh, es);
+  auto narrow = [&v](int w) { v = w < v ? w : v; };
+  if (q.x) narrow(rope_vec(q.x, T, H, q.xt, q.xh, es));
+  if (q.dy) narrow(rope_vec(q.dy, T, H, q.dt, q.dh, es));
+  narrow(rope_vec(q.wq, 1, 1, 0, 0, es));
+  narrow(rope_vec(q.wk, 1, 1, 0, 0, es));
+  RopePlan p;
+  const bool inter = layout == GBN_ROPE_INTERLEAVED;
+  if (!rope_plan(T, H, HQ, D, rot, inter, dtype, v, *dev, &p)) return GBN_EINVAL;
+  if (dir == 1 && q.wq != nullptr && ws_bytes < p.ws_bytes) return GBN_EWORKSPACE;
+  return to_status(rope_launch(p, q, dir, dtype, T, H, HQ, D, rot, inter, scale, eps,
+                               static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
+
+// --------------------------------- head RMSNorm and rotary positions --
+
+int gbn_norm_rope_forward(const void* x, int dtype, int64_t T, int64_t H, int64_t q_heads,
+                          int64_t D, int64_t x_token, int64_t x_head, const void* positions,
+                          int pos_bits, const uint64_t* freqs, int64_t rot, int layout,
+                          float scale, const void* wq, const void* wk, float eps, void* y,
+                          int64_t y_token, int64_t y_head, float* rstd, void* stream) {
+  const int rc = rope_check(dtype, T, H, q_heads, D, rot, layout, scale);
+  if (rc != GBN_OK) return rc;
+  if (!(eps >= 0.f) || (pos_bits != 32 && pos_bits != 64)) return GBN_EINVAL;
+  if (!rope_strides(T, H, D, x_token, x_head) || !rope_strides(T, H, D, y_token, y_head))
+    return GBN_EINVAL;
+  if (T == 0 || H == 0) return GBN_OK;
+  if (x == nullptr || y == nullptr) return GBN_EINVAL;
+  if (rot > 0 && (positions == nullptr || freqs == nullptr)) return GBN_EINVAL;
+  if (wq != nullptr && q_heads < H && wk == nullptr) return GBN_EINVAL;
+  if (wq == nullptr && wk != nullptr) return GBN_EINVAL;
+  if (!aligned(freqs, 8) || !aligned(positions, pos_bits / 8)) return GBN_EALIGN;
+  RopePtrs q;
+  q.x = x;
+  q.out = y;
+  q.pos = positions;
+  q.pos64 = pos_bits == 64;
+  q.freqs = freqs;
+  q.wq = wq;
+  q.wk = wk;
+  q.rstd = rstd;
+  q.xt = x_token;
+  q.xh = x_head;
+  q.yt = y_token;
+  q.yh = y_head;
+  return rope_call(q, 0, dtype, T, H, q_heads, D, rot, layout, scale, eps, 0, stream);
+}
+
+size_t gbn_norm_rope_workspace_bytes(int64_t T, int64_t H, int64_t q_heads, int64_t D, int64_t rot,
+                                     int dtype, int device) {
+  if (rope_check(dtype, T, H, q_heads, D, rot, GBN_ROPE_HALF, 1.f) != GBN_OK) return 0;
+  if (T == 0 || H == 0) return 256;
+  const DevInfo* dev = device_info(device);
+  if (!dev) return 0;
+  return rope_ws_bound(T, H, q_heads, D, rot, dtype, *dev);
+}
+
+int gbn_norm_rope_backward(const void* dy, const void* x, int dtype, int64_t T, int64_t H,
+                           int64_t q_heads, int64_t D, int64_t dy_token, int64_t dy_head,
+                           int64_t x_token, int64_t x_head, const void* positions, int pos_bits,
+                           const uint64_t* freqs, int64_t rot, int layout, float scale,
+                           const float* rstd, const void* wq, const void* wk, void* dx,
+                           int64_t dx_token, int64_t dx_head, void* dwq, void* dwk, void* ws,
+                           size_t ws_bytes, void* stream) {
+  const int rc = rope_check(dtype, T, H, q_heads, D, rot, layout, scale);
+  if (rc != GBN_OK) return rc;
+  if (pos_bits != 32 && pos_bits != 64) return GBN_EINVAL;
+  const bool norm = wq != nullptr;
+  if (!rope_strides(T, H, D, dy_token, dy_head) || !rope_strides(T, H, D, dx_token, dx_head) ||
+      (norm && !rope_strides(T, H, D, x_token, x_head)))
+    return GBN_EINVAL;
+  if (norm && q_heads < H && wk == nullptr) return GBN_EINVAL;
+  if (!norm && (wk != nullptr || dwq != nullptr || dwk != nullptr)) return GBN_EINVAL;
+  if (H == 0 || (T == 0 && !norm)) return GBN_OK;
+  if (T > 0) {
+    if (dy == nullptr || dx == nullptr) return GBN_EINVAL;
+    if (norm && (x == nullptr || rstd == nullptr || ws == nullptr)) return GBN_EINVAL;
+    if (rot > 0 && (positions == nullptr || freqs == nullptr)) return GBN_EINVAL;
+  }
+  if (!aligned(freqs, 8) || !aligned(positions, pos_bits / 8) || !aligned(ws, 16))
+    return GBN_EALIGN;
+  RopePtrs q;
+  q.x = norm ? x : nullptr;
+  q.dy = dy;
+  q.out = dx;
+  q.pos = positions;
+  q.pos64 = pos_bits == 64;
+  q.freqs = freqs;
+  q.wq = wq;
+  q.wk = wk;
+  q.rstd = const_cast<float*>(rstd);
+  q.dwq = dwq;
+  q.dwk = dwk;
+  q.ws = ws;
+  q.xt = x_token;
+  q.xh = x_head;
+  q.yt = dx_token;
+  q.yh = dx_head;
+  q.dt = dy_token;
+  q.dh = dy_head;
+  return rope_call(q, 1, dtype, T, H, q_heads, D, rot, layout, scale, 0.f, T == 0 ? (size_t)-1 : ws_bytes,
+                   stream);
+}
 
 // ------------------------------------------- GroupNorm, channels last --
 

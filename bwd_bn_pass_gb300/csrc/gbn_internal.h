@@ -327,6 +327,43 @@ cudaError_t gn_backward(const GnPlan& p, int dtype, const void* x, const void* d
                         float slope, void* dx, float* dgamma, float* dbeta, void* ws,
                         cudaStream_t st);
 
+// ------------------------------- head RMSNorm and rotary positions --
+
+constexpr int64_t kRopeMaxD = 512;  // head dimension
+
+struct RopePlan {
+  int vec = 1;        // elements per vector
+  int ns = 1;         // slots (pairs of vectors) per lane
+  int L = 1;          // lanes per team
+  int hc = 1;         // forward: heads per chunk
+  int cq = 0, ck = 0; // backward: chunks of query / key heads
+  int64_t bx = 1;     // backward: blocks per chunk
+  size_t ws_bytes = 0;
+};
+struct RopePtrs {
+  const void* x = nullptr;
+  const void* dy = nullptr;
+  void* out = nullptr;
+  const void* pos = nullptr;
+  bool pos64 = true;
+  const uint64_t* freqs = nullptr;
+  const void* wq = nullptr;  // null: no norm
+  const void* wk = nullptr;
+  float* rstd = nullptr;
+  void* dwq = nullptr;
+  void* dwk = nullptr;
+  void* ws = nullptr;
+  int64_t xt = 0, xh = 0, yt = 0, yh = 0, dt = 0, dh = 0;  // token / head strides
+};
+bool rope_plan(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, bool inter, int dtype,
+               int vec_max, const DevInfo& dev, RopePlan* p);
+size_t rope_ws_bound(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, int dtype,
+                     const DevInfo& dev);
+// dir: 0 forward, 1 backward (without wq: the rotation back of dy).
+cudaError_t rope_launch(const RopePlan& p, const RopePtrs& q, int dir, int dtype, int64_t T,
+                        int64_t H, int64_t HQ, int64_t D, int64_t rot, bool inter, float scale,
+                        float eps, cudaStream_t st);
+
 // ------------------------------------------ dropout, mask never stored --
 
 constexpr int kDBlocksPerSm = 4;  // 256-thread blocks per SM the grid fills

@@ -109,6 +109,12 @@ _SIGNATURES = {
                                          _P, _P, _P, _SZ, _P]),
     "gbn_gn_nhwc_backward": (_INT, [_P, _P, _INT, _I64, _I64, _I64, _I64, _P, _P, _P, _INT, _F,
                                     _P, _P, _P, _P, _SZ, _P]),
+    "gbn_norm_rope_forward": (_INT, [_P, _INT] + [_I64] * 6 + [_P, _INT, _P, _I64, _INT, _F, _P, _P,
+                                                               _F, _P, _I64, _I64, _P, _P]),
+    "gbn_norm_rope_workspace_bytes": (_SZ, [_I64] * 5 + [_INT, _INT]),
+    "gbn_norm_rope_backward": (_INT, [_P, _P, _INT] + [_I64] * 8
+                               + [_P, _INT, _P, _I64, _INT, _F, _P, _P, _P, _P, _I64, _I64, _P, _P,
+                                  _P, _SZ, _P]),
     "gbn_dropout_forward": (_INT, [_P, _INT, _I64, _I64, _P, _P, _D, _U64, _U64, _P, _P, _P]),
     "gbn_dropout_workspace_bytes": (_SZ, [_I64, _I64, _INT, _INT]),
     "gbn_dropout_backward": (_INT, [_P, _INT, _I64, _I64, _D, _U64, _U64, _P, _P, _P, _P, _SZ,
@@ -774,6 +780,174 @@ def gn_nhwc_backward(x, dy, stats, gamma=None, beta=None, *, act=None, slope=0.0
             ws.numel() * ws.element_size(), _stream(x.device))
     _check("gbn_gn_nhwc_backward", st)
     return dx, dgamma, dbeta
+
+
+# ------------------------------------- head RMSNorm and rotary positions --
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rope_inv_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_length=None,
+                         turns=(1.0, 32.0)):
+    """The angle per position of every pair of the first ``rot`` elements, a
+    float64 CPU tensor [rot / 2]: ``base ** (-2 i / rot)``, scaled for contexts
+    ``factor`` times longer than the trained one:
+
+    * None: not scaled;
+    * "linear": every angle divided by ``factor`` (positions interpolated);
+    * "base": base * factor ** (rot / (rot - 2)), which leaves the fastest
+      pair alone and divides the slowest one by ``factor``;
+    * "ramp": pairs that turn more than ``turns[1]`` times within
+      ``original_length`` positions stay, those below ``turns[0]`` are divided
+      by ``factor``, linear in the number of turns between."""
+    if rot % 2 or rot < 2:
+        raise ValueError("rot must be even and positive")
+    if scaling not in (None, "linear", "base", "ramp"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'ramp'")
+    if not factor > 0 or not base > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling == "base":
+        if rot == 2:
+            raise ValueError("scaling the base needs more than one pair")
+        base = base * factor ** (rot / (rot - 2))
+    inv = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "ramp":
+        if original_length is None or not turns[0] < turns[1]:
+            raise ValueError("ramp scaling needs original_length and rising turns")
+        n = original_length * inv / (2 * math.pi)
+        keep = ((n - turns[0]) / (turns[1] - turns[0])).clamp(0.0, 1.0)
+        inv = inv * keep + inv / factor * (1.0 - keep)
+    return inv
+
+
+def rope_frequencies(inv_freq, device=None):
+    """The frequency table that the rotary calls take, made once from the
+    angles per position (radians, any float tensor; see
+    ``rope_inv_frequencies``): each pair's fraction of a turn per position in
+    0.64 fixed point, an int64 tensor on ``device`` (default: inv_freq's)."""
+    inv = inv_freq.to(torch.float64)
+    if inv.dim() != 1 or not bool(torch.isfinite(inv).all()):
+        raise ValueError("inv_freq must be a finite vector")
+    t = inv / (2 * math.pi)
+    t = (t - t.floor()) * 2.0 ** 32
+    hi = t.floor()
+    lo = ((t - hi) * 2.0 ** 32).floor()
+    return ((hi.to(torch.int64) << 32) | lo.to(torch.int64)).to(device or inv_freq.device)
+
+
+def _rope_rows(t, name, shape=None):
+    """A [T, H, D] CUDA tensor whose last dimension is contiguous; its token
+    and head strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens, heads, D] with a contiguous last dimension")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    return t.stride(0), t.stride(1)
+
+
+def _rope_args(x, positions, freqs, wq, wk, q_heads, layout):
+    T, H, D = x.shape
+    q_heads = H if q_heads is None else int(q_heads)
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    if _cuda(positions, "positions").dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64")
+    if positions.numel() != T:
+        raise ValueError("positions must have one value per token")
+    if _cuda(freqs, "freqs").dtype != torch.int64:
+        raise TypeError("freqs must be the table of rope_frequencies")
+    for name, w in (("wq", wq), ("wk", wk)):
+        _col_vec(w, x, D, name)
+    if wq is None:
+        wk = None
+    elif wk is None and q_heads < H:
+        raise ValueError("heads from q_heads on need wk")
+    _same_device(x, ("positions", positions), ("freqs", freqs), ("wq", wq), ("wk", wk))
+    return (T, H, q_heads, D, 64 if positions.dtype == torch.int64 else 32, 2 * freqs.numel(),
+            _ROPE_LAYOUTS[layout], wk)
+
+
+def norm_rope_forward(x, positions, freqs, wq=None, wk=None, *, q_heads=None, eps=1e-5,
+                      layout="half", scale=1.0, y=None, rstd=None, want_rstd=True):
+    """RMSNorm of every head (weight ``wq`` for heads below ``q_heads``, ``wk``
+    for the rest; no norm without ``wq``) followed by rotary positions.
+
+    x: [tokens, heads, D], any token and head strides (a slice of a packed
+    projection); positions: int32 / int64 [tokens]; freqs: the table of
+    ``rope_frequencies``, whose length gives how much of a head turns.
+    Returns (y, rstd) -- y contiguous unless given (y=x turns in place), rstd
+    fp32 [tokens, heads] for the backward, or None without a norm or with
+    ``want_rstd=False``."""
+    xs = _rope_rows(x, "x")
+    T, H, hq, D, bits, rot, lay, wk = _rope_args(x, positions, freqs, wq, wk, q_heads, layout)
+    if y is None:
+        y = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    elif y.dtype != x.dtype:
+        raise ValueError("y must match x's dtype")
+    ys = _rope_rows(y, "y", x.shape)
+    if wq is None:
+        rstd = None
+    elif rstd is None and want_rstd:
+        rstd = torch.empty((T, H), dtype=torch.float32, device=x.device)
+    _fp32_vec(rstd, "rstd", T * H)
+    _same_device(x, ("y", y), ("rstd", rstd))
+    with torch.cuda.device(x.device):
+        st = lib().gbn_norm_rope_forward(
+            _ptr(x), _code(x.dtype), T, H, hq, D, *xs, _ptr(positions), bits, _ptr(freqs), rot, lay,
+            float(scale), _ptr(wq), _ptr(wk), float(eps), _ptr(y), *ys, _ptr(rstd),
+            _stream(x.device))
+    _check("gbn_norm_rope_forward", st)
+    return y, rstd
+
+
+def norm_rope_workspace(x, q_heads, rot):
+    T, H, D = x.shape
+    with torch.cuda.device(x.device):
+        n = lib().gbn_norm_rope_workspace_bytes(T, H, q_heads, D, rot, _code(x.dtype), -1)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
+
+
+def norm_rope_backward(dy, x, positions, freqs, rstd=None, wq=None, wk=None, *, q_heads=None,
+                       layout="half", scale=1.0, dx=None, dwq=None, dwk=None, ws=None):
+    """Backward of ``norm_rope_forward`` with the same arguments, from its
+    ``rstd``.  Returns (dx, dwq, dwk): dx contiguous unless given (a slice of
+    the packed gradient), dwq / dwk None where there is no such weight.
+    Without ``wq``, x and rstd are not read (x may be None)."""
+    ds = _rope_rows(dy, "dy")
+    T, H, hq, D, bits, rot, lay, wk = _rope_args(dy, positions, freqs, wq, wk, q_heads, layout)
+    xs = (0, 0)
+    if wq is not None:
+        xs = _rope_rows(x, "x", dy.shape)
+        if x.dtype != dy.dtype:
+            raise ValueError("dy must match x's dtype")
+        if rstd is None:
+            raise ValueError("rstd is required with a norm")
+        _fp32_vec(rstd, "rstd", T * H)
+        dwq = torch.empty_like(wq) if dwq is None else dwq
+        dwk = torch.empty_like(wk) if dwk is None and wk is not None else dwk
+        _col_vec(dwq, dy, D, "dwq")
+        _col_vec(dwk, dy, D, "dwk")
+        ws = norm_rope_workspace(dy, hq, rot) if ws is None else _cuda(ws, "ws")
+    elif dwq is not None or dwk is not None:
+        raise ValueError("weight gradients without weights")
+    if dx is None:
+        dx = torch.empty((T, H, D), dtype=dy.dtype, device=dy.device)
+    elif dx.dtype != dy.dtype:
+        raise ValueError("dx must match dy's dtype")
+    os_ = _rope_rows(dx, "dx", dy.shape)
+    _same_device(dy, ("x", x), ("rstd", rstd), ("dx", dx), ("dwq", dwq), ("dwk", dwk), ("ws", ws))
+    with torch.cuda.device(dy.device):
+        st = lib().gbn_norm_rope_backward(
+            _ptr(dy), _ptr(x), _code(dy.dtype), T, H, hq, D, *ds, *xs, _ptr(positions), bits,
+            _ptr(freqs), rot, lay, float(scale), _ptr(rstd), _ptr(wq), _ptr(wk), _ptr(dx), *os_,
+            _ptr(dwq), _ptr(dwk), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+            _stream(dy.device))
+    _check("gbn_norm_rope_backward", st)
+    return dx, dwq, dwk
 
 
 # ------------------------------------------- dropout, mask never stored --

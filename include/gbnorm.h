@@ -515,6 +515,53 @@ GBN_API int gbn_gn_nhwc_backward(const void* x, const void* dy, int dtype, int64
                                  float* dbeta, void* ws, size_t ws_bytes, void* stream);
 
 /* =========================================================================
+ * RMSNorm of every query / key head followed by rotary positions.
+ *
+ * x[t, h, 0..D) in `dtype`, T tokens, H heads, D <= 512 contiguous elements a
+ * row; token and head strides in elements (the heads of a packed projection
+ * are taken where they lie; at least D where there is more than one token or
+ * head).  Heads below q_heads (1 <= q_heads <= H) take the weight wq [D], the
+ * others wk [D].  wq NULL: no norm (rotary positions alone).
+ *   rstd[t,h] = 1/sqrt(mean_j x^2 + eps),  u = x*rstd*w,
+ *   y: pair i < rot/2 of u turned by positions[t]*f_i and multiplied by
+ *      `scale`, (p, q) -> scale*(p cos - q sin, q cos + p sin); elements from
+ *      rot on pass.  Pairs: GBN_ROPE_HALF (i, i + rot/2), GBN_ROPE_INTERLEAVED
+ *      (2i, 2i + 1).  rot even, 0 <= rot <= D.
+ * positions: int32 or int64 [T] (pos_bits 32 or 64; negative ones turn back).
+ * freqs: uint64 [rot/2], f_i / (2 pi) modulo 1 times 2^64: the angle of any
+ * 64-bit position modulo a turn comes out exact, with no table of sines.
+ * y may be x itself (same strides).
+ * ======================================================================= */
+#define GBN_ROPE_HALF 0
+#define GBN_ROPE_INTERLEAVED 1
+
+/* rstd: fp32 [T, H] or NULL (not written; a decoding step needs none).      */
+GBN_API int gbn_norm_rope_forward(const void* x, int dtype, int64_t T, int64_t H,
+                                  int64_t q_heads, int64_t D, int64_t x_token, int64_t x_head,
+                                  const void* positions, int pos_bits, const uint64_t* freqs,
+                                  int64_t rot, int layout, float scale, const void* wq,
+                                  const void* wk, float eps, void* y, int64_t y_token,
+                                  int64_t y_head, float* rstd, void* stream);
+
+/* Workspace bytes of the backward with the norm (-1: current device).       */
+GBN_API size_t gbn_norm_rope_workspace_bytes(int64_t T, int64_t H, int64_t q_heads, int64_t D,
+                                             int64_t rot, int dtype, int device);
+
+/* From the forward's rstd: g = the pairs of dy turned back (and multiplied by
+ * scale), dw_j = sum g*x*rstd over tokens and that weight's heads (dwq, dwk
+ * [D] in `dtype`, each may be NULL; dwk is 0 where there are no key heads),
+ * dx = rstd*(g*w - x*rstd*mean_j(g*w*x*rstd)).  Without wq: dx = g; x, rstd,
+ * dwq, dwk and ws are not used and the weight gradients must be NULL.
+ * dx may be dy or x itself (same strides).                                  */
+GBN_API int gbn_norm_rope_backward(const void* dy, const void* x, int dtype, int64_t T, int64_t H,
+                                   int64_t q_heads, int64_t D, int64_t dy_token, int64_t dy_head,
+                                   int64_t x_token, int64_t x_head, const void* positions,
+                                   int pos_bits, const uint64_t* freqs, int64_t rot, int layout,
+                                   float scale, const float* rstd, const void* wq, const void* wk,
+                                   void* dx, int64_t dx_token, int64_t dx_head, void* dwq,
+                                   void* dwk, void* ws, size_t ws_bytes, void* stream);
+
+/* =========================================================================
  * Dropout from a counter-based generator: the mask is drawn where it is used
  * and never stored.
  *

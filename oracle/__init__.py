@@ -41,6 +41,7 @@ from .layernorm import (
     layer_norm_backward_saved_z,
 )
 from .groupnorm import group_norm_act, group_norm_act_gate, group_norm_forward, group_norm_backward
+from .rope import norm_rope_forward, norm_rope_backward
 from .dropout import (
     philox4x32_10,
     dropout_threshold,
@@ -74,6 +75,8 @@ __all__ = [
     "group_norm_act_gate",
     "group_norm_forward",
     "group_norm_backward",
+    "norm_rope_forward",
+    "norm_rope_backward",
     "philox4x32_10",
     "dropout_threshold",
     "dropout_scale",
