@@ -1,0 +1,383 @@
+"""Head RMSNorm with rotary positions: the oracle against autograd and
+differences, the frequency table, refusals, and the CUDA path against the
+float64 oracle over layouts, odd sizes, strides and far positions.
+
+Tolerances.  With u the normed row, an output element is scale*(p cos - q sin):
+the angle (1/2 step of fp32 of at most half a turn, 2^-25 pi) and sincospi (2
+steps) leave at most 4 * 2^-24 of |p| + |q| each way, rounding in u (four
+products and a root) at most 6 * 2^-24 more, so fp32 results lie within
+16 * 2^-24 * (|p| + |q|); bf16 adds half a step of the result, 2^-8.  The
+weight gradients sum N such terms: 32 * 2^-24 * sum |terms| (2^-8 of the
+result more in bf16), the row mean in dx adds as much of its own terms."""
+
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+DEV = "cuda:0"
+OK, EINVAL, EDTYPE, EALIGN, EWORKSPACE = 0, -1, -2, -3, -4
+P = ctypes.c_void_p
+A16, A4, A2 = P(0x10000), P(0x10004), P(0x10002)
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+E32 = 2.0 ** -24
+
+
+def _table(gbn, rot, **kw):
+    return gbn.rope_frequencies(gbn.rope_inv_frequencies(rot, **kw))
+
+
+def _u64(t):
+    return [int(v) & 0xFFFFFFFFFFFFFFFF for v in t.cpu().tolist()]
+
+
+# ------------------------------------------------------------- the oracle
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_oracle_matches_autograd(gbn, layout):
+    g = torch.Generator().manual_seed(1)
+    T, H, D, rot = 5, 3, 10, 6
+    x = torch.randn(T, H, D, generator=g, dtype=torch.float64, requires_grad=True)
+    wq, wk = (torch.randn(D, generator=g, dtype=torch.float64, requires_grad=True) for _ in "qk")
+    dy = torch.randn(T, H, D, generator=g, dtype=torch.float64)
+    pos = torch.tensor([0, 1, 7, -3, 100000])
+    inv = gbn.rope_inv_frequencies(rot)
+    ang = pos.double()[:, None] * inv
+    w = torch.stack([wq, wq, wk])
+    u = x * (x.square().mean(-1, keepdim=True) + 1e-5).rsqrt() * w
+    i = torch.arange(rot // 2)
+    a, b = (i, i + rot // 2) if layout == "half" else (2 * i, 2 * i + 1)
+    c, s = ang.cos()[:, None], ang.sin()[:, None]
+    y = u.clone()
+    y[..., a] = 1.5 * (u[..., a] * c - u[..., b] * s)
+    y[..., b] = 1.5 * (u[..., b] * c + u[..., a] * s)
+    y.backward(dy)
+    n = [t.detach().numpy() for t in (x, wq, wk, dy)]
+    f = _u64(gbn.rope_frequencies(inv))
+    fw = oracle.norm_rope_forward(n[0], pos, f, n[1], n[2], 2, 1e-5, layout, 1.5)
+    bw = oracle.norm_rope_backward(n[3], n[0], pos, f, fw["rstd"], n[1], n[2], 2, layout, 1.5)
+    # 100000 turns of a frequency in 53 bits: 1e-11 of an angle
+    np.testing.assert_allclose(fw["y"], y.detach().numpy(), rtol=1e-9, atol=1e-9)
+    for k, t in (("dx", x), ("dwq", wq), ("dwk", wk)):
+        np.testing.assert_allclose(bw[k], t.grad.numpy(), rtol=1e-9, atol=1e-9)
+
+
+def test_oracle_matches_differences():
+    g = np.random.default_rng(2)
+    x, dy, w = g.normal(size=(2, 1, 6)), g.normal(size=(2, 1, 6)), g.normal(size=6)
+    f = [1 << 60, 12345678901234567]
+
+    def loss(xx):
+        return (oracle.norm_rope_forward(xx, [3, 9], f, w)["y"] * dy).sum()
+
+    fw = oracle.norm_rope_forward(x, [3, 9], f, w)
+    bw = oracle.norm_rope_backward(dy, x, [3, 9], f, fw["rstd"], w)
+    for i in np.ndindex(x.shape):
+        e = np.zeros_like(x)
+        e[i] = 1e-6
+        assert abs((loss(x + e) - loss(x - e)) / 2e-6 - bw["dx"][i]) < 1e-7
+
+
+def test_frequencies(gbn):
+    inv = gbn.rope_inv_frequencies(8, 10000.0)
+    np.testing.assert_allclose(inv.numpy(), [1.0, 0.1, 0.01, 0.001], rtol=1e-14)
+    np.testing.assert_allclose(gbn.rope_inv_frequencies(8, scaling="linear", factor=4.0),
+                               inv / 4, rtol=1e-14)
+    b = gbn.rope_inv_frequencies(8, scaling="base", factor=4.0)
+    assert b[0] == 1.0 and abs(float(b[-1] / inv[-1]) - 0.25) < 1e-12
+    r = gbn.rope_inv_frequencies(64, scaling="ramp", factor=8.0, original_length=4096)
+    plain = gbn.rope_inv_frequencies(64)
+    n = 4096 * plain / (2 * math.pi)
+    assert torch.equal(r[n >= 32], plain[n >= 32])
+    np.testing.assert_allclose(r[n <= 1], plain[n <= 1] / 8, rtol=1e-14)
+    assert bool((r <= plain).all()) and bool((r >= plain / 8 * (1 - 1e-12)).all())
+    t = gbn.rope_frequencies(torch.tensor([2 * math.pi * 0.25, 2 * math.pi * 0.75, 0.0,
+                                           -2 * math.pi * 0.25], dtype=torch.float64))
+    assert _u64(t)[0] == 1 << 62 and _u64(t)[1] == 3 << 62 and _u64(t)[2] == 0
+    assert abs(_u64(t)[3] - (3 << 62)) < 1 << 12
+    for bad in (dict(rot=7), dict(rot=0), dict(rot=8, scaling="x"), dict(rot=8, factor=0.0),
+                dict(rot=8, scaling="ramp"), dict(rot=2, scaling="base")):
+        with pytest.raises(ValueError):
+            gbn.rope_inv_frequencies(**bad)
+    with pytest.raises(ValueError):
+        gbn.rope_frequencies(torch.tensor([float("nan")]))
+
+
+# --------------------------------------------------------------- refusals
+
+def test_argument_errors(gbn):
+    L = gbn.lib()
+
+    def fwd(x=A16, dtype=0, T=2, H=3, hq=2, D=8, xt=24, xh=8, pos=A16, bits=64, f=A16, rot=8,
+            lay=0, scale=1.0, wq=A16, wk=A16, eps=1e-5, y=A16, yt=24, yh=8):
+        return L.gbn_norm_rope_forward(x, dtype, T, H, hq, D, xt, xh, pos, bits, f, rot, lay, scale,
+                                       wq, wk, eps, y, yt, yh, None, None)
+
+    def bwd(dy=A16, x=A16, dtype=0, T=2, H=3, hq=2, D=8, dt=24, dh=8, xt=24, xh=8, pos=A16, bits=64,
+            f=A16, rot=8, lay=0, scale=1.0, rstd=A16, wq=A16, wk=A16, dx=A16, ot=24, oh=8, dwq=A16,
+            dwk=A16, ws=A16, n=1 << 24):
+        return L.gbn_norm_rope_backward(dy, x, dtype, T, H, hq, D, dt, dh, xt, xh, pos, bits, f, rot,
+                                        lay, scale, rstd, wq, wk, dx, ot, oh, dwq, dwk, ws, n, None)
+
+    for c in (fwd, bwd):
+        assert c(dtype=4) == EDTYPE
+        for kw in ({"T": -1}, {"H": -1}, {"H": 70000}, {"D": 0}, {"D": 513, "xh": 600}, {"hq": 0},
+                   {"hq": 4}, {"rot": 7}, {"rot": 10}, {"rot": -2}, {"lay": 2},
+                   {"scale": float("inf")}, {"bits": 16}, {"xh": 7}, {"xt": 0}, {"xt": -24},
+                   {"pos": None}, {"f": None}, {"wk": None}, {"x": None}, {"T": 1 << 50}):
+            assert c(**kw) == EINVAL, kw
+        assert c(f=A4) == EALIGN
+        assert c(pos=A4) == EALIGN
+        assert c(pos=A2, bits=32) == EALIGN
+    for kw in ({"eps": -1.0}, {"eps": float("nan")}, {"y": None}, {"yh": 4}, {"wq": None}):
+        assert fwd(**kw) == EINVAL, kw
+    assert fwd(T=0) == OK
+    for kw in ({"dy": None}, {"dx": None}, {"rstd": None}, {"ws": None}, {"oh": 4}, {"dt": 3},
+               {"wq": None}):
+        assert bwd(**kw) == EINVAL, kw
+    assert bwd(wq=None, wk=None) == EINVAL      # weight gradients without weights
+    assert bwd(ws=A4) == EALIGN
+    assert bwd(T=0, wq=None, wk=None, dwq=None, dwk=None) == OK
+
+
+def test_binding_refusals(gbn):
+    x = torch.zeros(2, 3, 8)
+    with pytest.raises(ValueError):
+        gbn.norm_rope_forward(x, torch.arange(2), _table(gbn, 8))
+
+
+# ----------------------------------------------------------------- the GPU
+
+@pytest.fixture
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return DEV
+
+
+def _f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def _pair_mag(v, rot, layout):
+    """|p| + |q| for every element of a turning pair, |v| elsewhere."""
+    i = np.arange(rot // 2)
+    a, b = (i, i + rot // 2) if layout == "half" else (2 * i, 2 * i + 1)
+    m = np.abs(v)
+    s = m[..., a] + m[..., b]
+    out = m.copy()
+    out[..., a], out[..., b] = s, s
+    return out
+
+
+def _near(got, ref, bound, dtype, what):
+    err = np.abs(_f64(got) - ref)
+    lim = bound + 1e-30 + (2.0 ** -8 * (np.abs(ref) + bound) if dtype == "bf16" else 0.0)
+    assert np.all(err <= lim), f"{what}: {np.max(err / lim)} of the bound"
+
+
+def _check(gbn, x, dy, pos, table, wq, wk, hq, layout, dtype, what, scale=1.0, **out):
+    rot = 2 * table.numel()
+    f = _u64(table)
+    y, rstd = gbn.norm_rope_forward(x, pos, table, wq, wk, q_heads=hq, layout=layout, scale=scale)
+    n = [_f64(t) for t in (x, wq, wk, dy)]
+    p = pos.cpu().tolist()
+    T, H, D = x.shape
+    ref = oracle.norm_rope_forward(n[0], p, f, n[1], n[2], hq, 1e-5, layout, scale)
+    u = n[0]
+    if wq is not None:
+        w = np.concatenate([np.broadcast_to(n[1], (hq, D)),
+                            np.broadcast_to(n[2] if n[2] is not None else n[1], (H - hq, D))])
+        u = n[0] * ref["rstd"][..., None] * w
+        np.testing.assert_allclose(_f64(rstd), ref["rstd"], rtol=8 * E32 * (1 + math.log2(D)))
+    else:
+        assert rstd is None
+    _near(y, ref["y"], (16 + math.log2(D)) * E32 * scale * _pair_mag(u, rot, layout), dtype,
+          what + " y")
+    dx, dwq, dwk = gbn.norm_rope_backward(dy, x, pos, table, rstd, wq, wk, q_heads=hq,
+                                          layout=layout, scale=scale, **out)
+    bw = oracle.norm_rope_backward(n[3], n[0], p, f, _f64(rstd), n[1], n[2], hq, layout, scale)
+    gm = scale * _pair_mag(n[3], rot, layout)
+    if wq is None:
+        _near(dx, bw["dx"], 16 * E32 * gm, dtype, what + " dx")
+        return y, dx
+    r = _f64(rstd)[..., None]
+    xh = np.abs(n[0] * r)
+    gw = gm * np.abs(w)
+    mean = (gw * xh).mean(axis=2, keepdims=True)
+    _near(dx, bw["dx"], 32 * E32 * r * (gw + xh * mean), dtype, what + " dx")
+    t = (gm * xh).sum(axis=0)
+    # plain fp32 sums (bf16 storage) of n terms are off by at most n steps
+    steps = 32 + (T * H if dtype == "bf16" else 0)
+    for k, got, terms in (("dwq", dwq, t[:hq].sum(axis=0)), ("dwk", dwk, t[hq:].sum(axis=0))):
+        if bw[k] is not None:
+            _near(got, bw[k], steps * E32 * terms, dtype, f"{what} {k}")
+    return y, dx, dwq, dwk
+
+
+def _case(gbn, T, HQ, HK, D, rot, dtype, seed, norm=True, far=False, packed=True):
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(T, HQ + 2 * HK + 1, D, generator=g).to(DT[dtype]).to(DEV)
+    x = qkv[:, :HQ + HK] if packed else qkv[:, :HQ + HK].contiguous()
+    dy = torch.randn(T, HQ + HK, D, generator=g).to(DT[dtype]).to(DEV)
+    pos = torch.randint(0, 1 << 40 if far else 5000, (T,), generator=g).to(DEV)
+    wq, wk = ((0.5 + torch.rand(D, generator=g)).to(DT[dtype]).to(DEV) if norm else None
+              for _ in "qk")
+    return x, dy, pos, _table(gbn, rot).to(DEV), wq, wk
+
+
+SHAPES = [  # T, HQ, HK, D, rot
+    (1, 1, 0, 2, 2), (3, 4, 2, 64, 64), (5, 2, 1, 128, 64), (2, 3, 3, 80, 80), (7, 1, 1, 96, 48),
+    (4, 5, 1, 10, 6), (3, 2, 2, 7, 4), (33, 8, 2, 128, 128), (2, 2, 1, 256, 256),
+    (3, 2, 0, 512, 512), (2, 1, 1, 510, 130), (6, 2, 1, 192, 30), (2, 3, 1, 320, 8),
+    (1, 40, 8, 128, 128), (70, 3, 1, 36, 12), (2, 1, 1, 511, 2),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_parity(gbn, dev, shape, dtype, layout):
+    T, HQ, HK, D, rot = shape
+    a = _case(gbn, T, HQ, HK, D, rot, dtype, sum(shape))
+    _check(gbn, *a[:6], HQ, layout, dtype, f"rope {shape} {dtype} {layout}")
+    a = _case(gbn, T, HQ, HK, D, rot, dtype, sum(shape) + 1, norm=False, far=True, packed=False)
+    _check(gbn, *a[:6], HQ, layout, dtype, f"rope only {shape} {dtype} {layout}", scale=0.75)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_tokens_and_repeats(gbn, dev, dtype):
+    """Several chunks of heads, blocks that stride over tokens; twice the same
+    bits; int32 positions give the same."""
+    x, dy, pos, table, wq, wk = _case(gbn, 3000, 16, 4, 64, 32, dtype, 3)
+    a = _check(gbn, x, dy, pos, table, wq, wk, 16, "half", dtype, "many")
+    b = _check(gbn, x, dy, pos.int(), table, wq, wk, 16, "half", dtype, "many")
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_strides_in_place_and_packed_gradient(gbn, dev):
+    x, dy, pos, table, wq, wk = _case(gbn, 9, 4, 2, 64, 64, "bf16", 5)
+    y, rstd = gbn.norm_rope_forward(x, pos, table, wq, wk, q_heads=4)
+    dx, dwq, dwk = gbn.norm_rope_backward(dy, x, pos, table, rstd, wq, wk, q_heads=4)
+    # head-major storage, odd (unaligned) strides
+    hm = x.transpose(0, 1).contiguous().transpose(0, 1)
+    odd = torch.zeros(9, 6, 67, dtype=x.dtype, device=dev)[:, :, 1:65]
+    odd.copy_(x)
+    for v in (hm, odd):
+        y2, r2 = gbn.norm_rope_forward(v, pos, table, wq, wk, q_heads=4)
+        assert torch.equal(y, y2)
+        torch.testing.assert_close(rstd, r2, rtol=1e-6, atol=0)
+        d2, _, _ = gbn.norm_rope_backward(dy, v, pos, table, rstd, wq, wk, q_heads=4)
+        torch.testing.assert_close(d2.float(), dx.float(), rtol=2 ** -7, atol=1e-5)
+    packed = torch.full((9, 9, 64), 7.0, dtype=x.dtype, device=dev)
+    gbn.norm_rope_backward(dy, x, pos, table, rstd, wq, wk, q_heads=4, dx=packed[:, :6])
+    assert torch.equal(packed[:, :6], dx) and bool((packed[:, 6:] == 7.0).all())
+    z = dy.clone()
+    assert torch.equal(gbn.norm_rope_backward(z, x, pos, table, rstd, wq, wk, q_heads=4, dx=z)[0], dx)
+    z = x.contiguous()
+    assert torch.equal(gbn.norm_rope_forward(z, pos, table, wq, wk, q_heads=4, y=z)[0], y)
+    n, r = gbn.norm_rope_forward(x, pos, table, wq, wk, q_heads=4, want_rstd=False)
+    assert r is None and torch.equal(n, y)
+
+
+@pytest.mark.gpu
+def test_far_negative_and_zero_positions(gbn, dev):
+    x, dy, _, table, wq, wk = _case(gbn, 6, 2, 0, 64, 64, "f32", 7)
+    pos = torch.tensor([0, -1, 2 ** 62 + 12345, -2 ** 62, 2 ** 31 + 7, 1], device=dev)
+    y, _ = _check(gbn, x, dy, pos, table, None, None, 2, "half", "f32", "far")
+    assert torch.equal(y[0], x[0])       # position 0 turns nothing
+    inv, _ = gbn.norm_rope_forward(y, -pos, table)
+    torch.testing.assert_close(inv, x, rtol=0, atol=64 * E32 * 4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_passing_elements_do_not_mix(gbn, dev, layout):
+    """Infinities and NaNs beyond rot (no norm) touch nothing else; pairs keep
+    theirs."""
+    x, _, pos, table, _, _ = _case(gbn, 4, 2, 0, 48, 12, "f32", 9, norm=False, packed=False)
+    y, _ = gbn.norm_rope_forward(x, pos, table, layout=layout)
+    z = x.clone()
+    z[..., 13::2] = float("inf")
+    z[..., 14::4] = float("nan")
+    y2, _ = gbn.norm_rope_forward(z, pos, table, layout=layout)
+    assert torch.equal(y2[..., :13], y[..., :13])
+    assert torch.equal(torch.nan_to_num(y2[..., 12:]), torch.nan_to_num(z[..., 12:]))
+
+
+@pytest.mark.gpu
+def test_no_rotation_zero_rows_and_empty(gbn, dev):
+    x, dy, pos, _, wq, wk = _case(gbn, 5, 3, 2, 64, 64, "f32", 11)
+    empty = torch.empty(0, dtype=torch.int64, device=dev)
+    _check(gbn, x, dy, pos, empty, wq, wk, 3, "half", "f32", "no rotation")
+    z = torch.zeros_like(x)
+    y, rstd = gbn.norm_rope_forward(z, pos, empty, wq, wk, q_heads=3)
+    assert not y.any() and bool(torch.isfinite(rstd).all())
+    e = torch.empty(0, 5, 64, device=dev)
+    tab = _table(gbn, 64).to(dev)
+    y, rstd = gbn.norm_rope_forward(e, pos[:0], tab, wq, wk, q_heads=3)
+    dx, dwq, dwk = gbn.norm_rope_backward(e, e, pos[:0], tab, rstd, wq, wk, q_heads=3)
+    assert y.numel() == 0 and not dwq.any() and not dwk.any()
+    with pytest.raises(ValueError):
+        gbn.norm_rope_forward(x.transpose(1, 2), pos, tab)
+    with pytest.raises(ValueError):
+        gbn.norm_rope_forward(x, pos[:2], tab)
+    with pytest.raises(ValueError):
+        gbn.norm_rope_forward(x, pos, tab, wq, q_heads=3)
+    with pytest.raises(TypeError):
+        gbn.norm_rope_forward(x, pos.float(), tab)
+    with pytest.raises(TypeError):
+        gbn.norm_rope_forward(x, pos, tab.double())
+    with pytest.raises(gbn.GbnError):
+        gbn.norm_rope_forward(x, pos, _table(gbn, 66).to(dev))
+    with pytest.raises(gbn.GbnError):
+        gbn.norm_rope_forward(x[:1].expand(5, 5, 64), pos, tab)
+
+
+@pytest.mark.gpu
+def test_other_stream_and_graph(gbn, dev):
+    x, dy, pos, table, wq, wk = _case(gbn, 16, 4, 2, 128, 128, "bf16", 13)
+    y, rstd = gbn.norm_rope_forward(x, pos, table, wq, wk, q_heads=4)
+    grads = gbn.norm_rope_backward(dy, x, pos, table, rstd, wq, wk, q_heads=4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y2, r2 = gbn.norm_rope_forward(x, pos, table, wq, wk, q_heads=4)
+        g2 = gbn.norm_rope_backward(dy, x, pos, table, r2, wq, wk, q_heads=4)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, y2) and all(torch.equal(p, q) for p, q in zip(grads, g2))
+    outs = [torch.zeros_like(t) for t in (y, rstd, *grads)]
+    ws = gbn.norm_rope_workspace(dy, 4, 128)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gbn.norm_rope_forward(x, pos, table, wq, wk, q_heads=4, y=outs[0], rstd=outs[1])
+        gbn.norm_rope_backward(dy, x, pos, table, outs[1], wq, wk, q_heads=4, dx=outs[2],
+                               dwq=outs[3], dwk=outs[4], ws=ws)
+    for _ in range(2):
+        for t in outs:
+            t.zero_()
+        ws.fill_(0xFF)
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(outs, (y, rstd, *grads)))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gbn, dev):
+    """Token and head offsets past 2^32 elements."""
+    T, H, D = 17, 2, 64
+    big = torch.zeros((1 << 32) + (1 << 20), dtype=torch.bfloat16, device=dev)
+    step = ((1 << 32) // (T - 1)) & ~7
+    x = big.as_strided((T, H, D), (step, 4096, 1))
+    x.normal_(generator=torch.Generator(dev).manual_seed(15))
+    pos = torch.arange(T, device=dev)
+    tab = _table(gbn, 64).to(dev)
+    y, _ = gbn.norm_rope_forward(x, pos, tab)
+    y2, _ = gbn.norm_rope_forward(x.contiguous(), pos, tab)
+    assert torch.equal(y, y2)
