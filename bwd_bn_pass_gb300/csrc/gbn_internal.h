@@ -311,11 +311,12 @@ struct GnPlan {
   int slices = 1;           // row slices per sample
   int threads = 32;         // block size
   int tile_groups = 1;      // groups a tile can touch, at most
-  int64_t blocks = 0;       // N * slices * tiles
+  int rps = 1;              // rows per slice
+  int64_t run = 1;          // samples per pair of launches
   size_t gpart_bytes = 0;   // group partials; the channel partials follow
   size_t ws_bytes = 0;
 };
-bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, bool backward,
+bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, int64_t esize, bool backward,
              const DevInfo& dev, GnPlan* p);
 // Workspace for any vector width and direction.
 size_t gn_ws_bound(int64_t N, int64_t S, int64_t C, int64_t G, const DevInfo& dev);

@@ -9,6 +9,7 @@ call fails, an exception is raised.
 """
 
 import ctypes
+import functools
 import math
 import os
 
@@ -152,16 +153,41 @@ def exported_symbols():
 # ------------------------------------------------------------- helpers --
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _check(fn, status):
     if status != GBN_OK:
         raise GbnError(fn, status)
+
+
+def _call(device, name, *args):
+    """Call an entry point whose last argument is the stream, with ``device``
+    current; raise on a nonzero status.  (The current device is switched only
+    where it is another one: the switch costs more than a small kernel.)"""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    if st != GBN_OK:
+        raise GbnError(name, st)
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(name, device_index, *args):
+    """A workspace size query (a function of the shape and the device)."""
+    return int(getattr(lib(), name)(*args, device_index))
+
+
+def _workspace(name, device, *args):
+    n = _ws_bytes(name, device.index, *args)
+    return torch.empty(n if n > 256 else 256, dtype=torch.uint8, device=device)
 
 
 def _cuda(t, name):
@@ -717,11 +743,7 @@ def _gn_act(act):
 
 def gn_nhwc_workspace(x, groups):
     N, S, C = _gn_dims(x, groups)
-    with torch.cuda.device(x.device):
-        n = lib().gbn_gn_nhwc_workspace_bytes(N, S, C, groups, -1)
-    if n == 0:
-        raise ValueError(f"bad channels-last GroupNorm shape {tuple(x.shape)}")
-    return torch.empty(n, dtype=torch.uint8, device=x.device)
+    return _workspace("gbn_gn_nhwc_workspace_bytes", x.device, N, S, C, groups)
 
 
 def gn_nhwc_forward_train(x, groups, gamma=None, beta=None, eps=1e-5, *, act=None, slope=0.01,
@@ -742,12 +764,9 @@ def gn_nhwc_forward_train(x, groups, gamma=None, beta=None, eps=1e-5, *, act=Non
         _fp32_vec(stats, "stats", 3 * N * groups)
     ws = gn_nhwc_workspace(x, groups) if ws is None else _cuda(ws, "ws")
     _same_device(x, ("y", y), ("stats", stats), ("ws", ws), ("gamma", gamma), ("beta", beta))
-    with torch.cuda.device(x.device):
-        st = lib().gbn_gn_nhwc_forward_train(
-            _ptr(x), _code(x.dtype), N, S, C, groups, _ptr(gamma), _ptr(beta), float(eps), code,
-            float(slope), _ptr(y), _ptr(stats), _ptr(ws), ws.numel() * ws.element_size(),
-            _stream(x.device))
-    _check("gbn_gn_nhwc_forward_train", st)
+    _call(x.device, "gbn_gn_nhwc_forward_train", _ptr(x), _code(x.dtype), N, S, C, groups,
+          _ptr(gamma), _ptr(beta), float(eps), code, float(slope), _ptr(y), _ptr(stats),
+          _ptr(ws), ws.numel() * ws.element_size())
     return y, stats
 
 
@@ -773,12 +792,9 @@ def gn_nhwc_backward(x, dy, stats, gamma=None, beta=None, *, act=None, slope=0.0
     ws = gn_nhwc_workspace(x, groups) if ws is None else _cuda(ws, "ws")
     _same_device(x, ("dy", dy), ("stats", stats), ("gamma", gamma), ("beta", beta), ("dx", dx),
                  ("dgamma", dgamma), ("dbeta", dbeta), ("ws", ws))
-    with torch.cuda.device(x.device):
-        st = lib().gbn_gn_nhwc_backward(
-            _ptr(x), _ptr(dy), _code(x.dtype), N, S, C, groups, _ptr(stats), _ptr(gamma),
-            _ptr(beta), code, float(slope), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
-            ws.numel() * ws.element_size(), _stream(x.device))
-    _check("gbn_gn_nhwc_backward", st)
+    _call(x.device, "gbn_gn_nhwc_backward", _ptr(x), _ptr(dy), _code(x.dtype), N, S, C, groups,
+          _ptr(stats), _ptr(gamma), _ptr(beta), code, float(slope), _ptr(dx), _ptr(dgamma),
+          _ptr(dbeta), _ptr(ws), ws.numel() * ws.element_size())
     return dx, dgamma, dbeta
 
 
@@ -895,20 +911,16 @@ def norm_rope_forward(x, positions, freqs, wq=None, wk=None, *, q_heads=None, ep
         rstd = torch.empty((T, H), dtype=torch.float32, device=x.device)
     _fp32_vec(rstd, "rstd", T * H)
     _same_device(x, ("y", y), ("rstd", rstd))
-    with torch.cuda.device(x.device):
-        st = lib().gbn_norm_rope_forward(
-            _ptr(x), _code(x.dtype), T, H, hq, D, *xs, _ptr(positions), bits, _ptr(freqs), rot, lay,
-            float(scale), _ptr(wq), _ptr(wk), float(eps), _ptr(y), *ys, _ptr(rstd),
-            _stream(x.device))
-    _check("gbn_norm_rope_forward", st)
+    _call(x.device, "gbn_norm_rope_forward", _ptr(x), _code(x.dtype), T, H, hq, D, *xs,
+          _ptr(positions), bits, _ptr(freqs), rot, lay, float(scale), _ptr(wq), _ptr(wk),
+          float(eps), _ptr(y), *ys, _ptr(rstd))
     return y, rstd
 
 
 def norm_rope_workspace(x, q_heads, rot):
     T, H, D = x.shape
-    with torch.cuda.device(x.device):
-        n = lib().gbn_norm_rope_workspace_bytes(T, H, q_heads, D, rot, _code(x.dtype), -1)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
+    return _workspace("gbn_norm_rope_workspace_bytes", x.device, T, H, q_heads, D, rot,
+                      _code(x.dtype))
 
 
 def norm_rope_backward(dy, x, positions, freqs, rstd=None, wq=None, wk=None, *, q_heads=None,
@@ -940,13 +952,10 @@ def norm_rope_backward(dy, x, positions, freqs, rstd=None, wq=None, wk=None, *, 
         raise ValueError("dx must match dy's dtype")
     os_ = _rope_rows(dx, "dx", dy.shape)
     _same_device(dy, ("x", x), ("rstd", rstd), ("dx", dx), ("dwq", dwq), ("dwk", dwk), ("ws", ws))
-    with torch.cuda.device(dy.device):
-        st = lib().gbn_norm_rope_backward(
-            _ptr(dy), _ptr(x), _code(dy.dtype), T, H, hq, D, *ds, *xs, _ptr(positions), bits,
-            _ptr(freqs), rot, lay, float(scale), _ptr(rstd), _ptr(wq), _ptr(wk), _ptr(dx), *os_,
-            _ptr(dwq), _ptr(dwk), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-            _stream(dy.device))
-    _check("gbn_norm_rope_backward", st)
+    _call(dy.device, "gbn_norm_rope_backward", _ptr(dy), _ptr(x), _code(dy.dtype), T, H, hq, D,
+          *ds, *xs, _ptr(positions), bits, _ptr(freqs), rot, lay, float(scale), _ptr(rstd),
+          _ptr(wq), _ptr(wk), _ptr(dx), *os_, _ptr(dwq), _ptr(dwk), _ptr(ws), 0 if ws is
+          None else ws.numel() * ws.element_size())
     return dx, dwq, dwk
 
 
@@ -988,18 +997,14 @@ def dropout_forward(x, p, rng, *, bias=None, residual=None, y=None):
     y = torch.empty_like(x) if y is None else _like(y, x, "y")
     _same_device(x, ("bias", bias), ("residual", residual), ("y", y))
     seed, offset, state = _rng(rng, x)
-    with torch.cuda.device(x.device):
-        st = lib().gbn_dropout_forward(_ptr(x), _code(x.dtype), R, H, _ptr(bias), _ptr(residual),
-                                       float(p), seed, offset, state, _ptr(y), _stream(x.device))
-    _check("gbn_dropout_forward", st)
+    _call(x.device, "gbn_dropout_forward", _ptr(x), _code(x.dtype), R, H, _ptr(bias),
+          _ptr(residual), float(p), seed, offset, state, _ptr(y))
     return y
 
 
 def dropout_workspace(dy):
     R, H = _rows(dy, "dy")
-    with torch.cuda.device(dy.device):
-        n = lib().gbn_dropout_workspace_bytes(R, H, _code(dy.dtype), -1)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=dy.device)
+    return _workspace("gbn_dropout_workspace_bytes", dy.device, R, H, _code(dy.dtype))
 
 
 def dropout_backward(dy, p, rng, *, want_dbias=False, dx=None, dbias=None, ws=None):
@@ -1015,11 +1020,9 @@ def dropout_backward(dy, p, rng, *, want_dbias=False, dx=None, dbias=None, ws=No
         ws = dropout_workspace(dy)
     _same_device(dy, ("dx", dx), ("dbias", dbias), ("ws", ws))
     seed, offset, state = _rng(rng, dy)
-    with torch.cuda.device(dy.device):
-        st = lib().gbn_dropout_backward(
-            _ptr(dy), _code(dy.dtype), R, H, float(p), seed, offset, state, _ptr(dx), _ptr(dbias),
-            _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(dy.device))
-    _check("gbn_dropout_backward", st)
+    _call(dy.device, "gbn_dropout_backward", _ptr(dy), _code(dy.dtype), R, H, float(p), seed,
+          offset, state, _ptr(dx), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel() *
+          ws.element_size())
     return dx, dbias
 
 
@@ -1046,12 +1049,9 @@ def layernorm_dropout_forward(x, residual, p, rng, gamma=None, beta=None, eps=1e
     _same_device(x, ("residual", residual), ("gamma", gamma), ("beta", beta), ("bias", bias),
                  ("y", y), ("z", z), ("mean", mean), ("rstd", rstd))
     seed, offset, state = _rng(rng, x)
-    with torch.cuda.device(x.device):
-        st = lib().gbn_layernorm_dropout_forward(
-            _ptr(x), _code(x.dtype), R, H, _ptr(residual), _ptr(bias), float(p), seed, offset,
-            state, _ptr(gamma), _ptr(beta), float(eps), _ptr(y), _ptr(z), _ptr(mean), _ptr(rstd),
-            _stream(x.device))
-    _check("gbn_layernorm_dropout_forward", st)
+    _call(x.device, "gbn_layernorm_dropout_forward", _ptr(x), _code(x.dtype), R, H,
+          _ptr(residual), _ptr(bias), float(p), seed, offset, state, _ptr(gamma),
+          _ptr(beta), float(eps), _ptr(y), _ptr(z), _ptr(mean), _ptr(rstd))
     return {"y": y, "z": z, "mean": mean, "rstd": rstd}
 
 
@@ -1089,18 +1089,17 @@ def layernorm_dropout_backward(dy, x, residual, mean, rstd, gamma, p, rng, *, bi
     dbeta = torch.empty_like(gamma) if dbeta is None else dbeta
     if dbias is None and want_dbias:
         dbias = torch.empty_like(gamma)
-    ws = rowwise_workspace(R, H, GBN_ROW_LN_FUSED, x.dtype, x.device) if ws is None else ws
+    if ws is None:
+        ws = _workspace("gbn_rowwise_workspace_bytes", x.device, R, H, GBN_ROW_LN_FUSED,
+                        _code(x.dtype))
     _same_device(x, ("dy", dy), ("residual", residual), ("mean", mean), ("rstd", rstd),
                  ("gamma", gamma), ("bias", bias), ("dz_extra", dz_extra), ("dx", dx),
                  ("dresidual", dresidual), ("dgamma", dgamma), ("dbeta", dbeta),
                  ("dbias", dbias), ("ws", ws))
     seed, offset, state = _rng(rng, x)
     flags = (GBN_LN_SAVED_Z if saved_z else 0) | (GBN_LN_DRES_F32 if dres_f32 else 0)
-    with torch.cuda.device(x.device):
-        st = lib().gbn_layernorm_dropout_backward(
-            _ptr(dy), _ptr(x), _code(x.dtype), _ptr(mean), _ptr(rstd), _ptr(gamma), R, H,
-            _ptr(residual), _ptr(bias), float(p), seed, offset, state, _ptr(dz_extra), _ptr(dx),
-            _ptr(dresidual), _ptr(dgamma), _ptr(dbeta), _ptr(dbias), _ptr(ws),
-            ws.numel() * ws.element_size(), flags, _stream(x.device))
-    _check("gbn_layernorm_dropout_backward", st)
+    _call(x.device, "gbn_layernorm_dropout_backward", _ptr(dy), _ptr(x), _code(x.dtype),
+          _ptr(mean), _ptr(rstd), _ptr(gamma), R, H, _ptr(residual), _ptr(bias), float(p),
+          seed, offset, state, _ptr(dz_extra), _ptr(dx), _ptr(dresidual), _ptr(dgamma),
+          _ptr(dbeta), _ptr(dbias), _ptr(ws), ws.numel() * ws.element_size(), flags)
     return {"dx": dx, "dresidual": dresidual, "dgamma": dgamma, "dbeta": dbeta, "dbias": dbias}
