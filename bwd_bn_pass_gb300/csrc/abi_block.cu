@@ -77,7 +77,8 @@ int rope_call(RopePtrs q, int dir, int dtype, int64_t T, int64_t H, int64_t HQ, 
   narrow(rope_vec(q.wk, 1, 1, 0, 0, es));
   RopePlan p;
   const bool inter = layout == GBN_ROPE_INTERLEAVED;
-  if (!rope_plan(T, H, HQ, D, rot, inter, dtype, v, *dev, &p)) return GBN_EINVAL;
+  if (!rope_plan(T, H, HQ, D, rot, inter, dtype, v, dir == 1 && q.wq != nullptr ? 1 : 0, *dev,
+                 &p)) return GBN_EINVAL;
   if (dir == 1 && q.wq != nullptr && ws_bytes < p.ws_bytes) return GBN_EWORKSPACE;
   return to_status(rope_launch(p, q, dir, dtype, T, H, HQ, D, rot, inter, scale, eps,
                                static_cast<cudaStream_t>(stream)));

@@ -86,20 +86,19 @@ template <typename T> struct ColSum {
   }
 };
 
-template <typename T, bool BWD, bool RES>
-__global__ void __launch_bounds__(kDThreads, sizeof(T) == 2 ? 4 : 3) dropout_rows_kernel(DropArgs a) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // rows in flight
+template <typename T, bool BWD, bool RES, bool STATE>
+__global__ void __launch_bounds__(kDThreads, 4) dropout_rows_kernel(const DropArgs a) {
+  constexpr int U = sizeof(T) == 2 ? (RES ? 2 : 4) : (RES ? 1 : 2);  // rows in flight
   using C8 = Chunk8<T>;
   extern __shared__ DF red[];  // [TY][TX][8] when sums are asked for
-  const int tx = threadIdx.x % a.TX, ty = threadIdx.x / a.TX;
+  const int ty = threadIdx.x / a.TX, tx = threadIdx.x - ty * a.TX;
   const int cv = blockIdx.x * a.TX + tx;
   const bool active = cv < a.Hc;
   const int64_t H = a.H;
   const int64_t r0 = a.R * blockIdx.y / a.slices, r1 = a.R * (blockIdx.y + 1) / a.slices;
-  const T* x = static_cast<const T*>(a.x);
-  const T* res = static_cast<const T*>(a.res);
-  T* y = static_cast<T*>(a.y);
-  const Philox g = philox_load(a.rng);
+  Philox<STATE> g;
+  g.load(a.rng);
+  const float scale = a.rng.scale;
   float b[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) b[e] = 0.f;
@@ -110,33 +109,42 @@ __global__ void __launch_bounds__(kDThreads, sizeof(T) == 2 ? 4 : 3) dropout_row
       c.load(static_cast<const T*>(a.bias) + (int64_t)cv * 8);
       c.get(b);
     }
-    for (int64_t r = r0 + ty; r < r1; r += (int64_t)U * a.TY) {
+    const int64_t first = r0 + ty, step = (int64_t)a.TY * H;
+    const T* x = static_cast<const T*>(a.x) + first * H + (int64_t)cv * 8;
+    const T* res = static_cast<const T*>(a.res) + first * H + (int64_t)cv * 8;
+    T* y = static_cast<T*>(a.y) + first * H + (int64_t)cv * 8;
+    uint64_t blk = (uint64_t)(first * a.Hc + cv);
+    const uint64_t bstep = (uint64_t)a.TY * a.Hc;
+    int64_t left = r1 > first ? (r1 - first + a.TY - 1) / a.TY : 0;
+    for (; left > 0; left -= U) {
       C8 cx[U], cr[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t ru = r + (int64_t)u * a.TY;
-        if (ru < r1) {
-          cx[u].load(x + ru * H + (int64_t)cv * 8);
-          if constexpr (RES) cr[u].load(res + ru * H + (int64_t)cv * 8);
+      for (int u = 0; u < U; ++u)
+        if (u < left) {
+          cx[u].load(x + u * step);
+          if constexpr (RES) cr[u].load(res + u * step);
         }
-      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t ru = r + (int64_t)u * a.TY;
-        if (ru >= r1) continue;
-        float f[8], v[8], o[8];
-        keep_factors<8>(g, (uint64_t)(ru * H + (int64_t)cv * 8), a.rng.thr, a.rng.scale, f);
+        if (u >= left) continue;
+        bool f[8];
+        float v[8], o[8];
+        g.template keep<8>(a.rng, blk << 3, f);
         cx[u].get(v);
         if constexpr (RES) cr[u].get(o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           // a dropped element is exactly 0 (or the residual), whatever x holds
-          const float t = f[e] != 0.f ? (BWD ? v[e] : v[e] + b[e]) : 0.f;
-          o[e] = RES ? fmaf(t, f[e], o[e]) : t * f[e];
+          const float t = f[e] ? (BWD ? v[e] : v[e] + b[e]) : 0.f;
+          o[e] = RES ? fmaf(t, scale, o[e]) : t * scale;
           if constexpr (BWD) sum[e].add(o[e]);
         }
-        C8::store(y + ru * H + (int64_t)cv * 8, o);
+        C8::store(y + u * step, o);
+        blk += bstep;
       }
+      x += U * step;
+      if constexpr (RES) res += U * step;
+      y += U * step;
     }
   }
   if constexpr (BWD) {
@@ -174,7 +182,8 @@ __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.res);
   T* y = static_cast<T*>(a.y);
-  const Philox g = philox_load(a.rng);
+  PhiloxAny g;
+  g.load(a.rng);
   const float b = !BWD && active && a.bias ? to_f32(static_cast<const T*>(a.bias)[j]) : 0.f;
   ColSum<T> sum;
   const int wr = threadIdx.x >> 5, wl = threadIdx.x & 31;
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
       }
     }
     if (r + wr < r1)
-      bits[wr][wl] = (uint8_t)keep_bits(g, ((uint64_t)((r + wr) * H + j0) >> 3) + wl, a.rng.thr);
+      bits[wr][wl] = (uint8_t)g.bits(a.rng, ((uint64_t)((r + wr) * H + j0) >> 3) + wl);
     __syncthreads();
     if (active) {
 #pragma unroll
@@ -217,31 +226,43 @@ __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
   }
 }
 
-template <typename T>
-cudaError_t launch_drop(const DropPlan& p, const DropArgs& a, bool bwd, cudaStream_t st) {
-  const dim3 grid((unsigned)p.gx, (unsigned)p.slices);
-  if (!p.fast)
-    return bwd ? launch(dropout_tile_kernel<T, true>, grid, dim3(kDThreads), 0, st, false, a)
-               : launch(dropout_tile_kernel<T, false>, grid, dim3(kDThreads), 0, st, false, a);
-  const dim3 block((unsigned)(p.TX * p.TY));
+template <typename T, bool STATE>
+cudaError_t launch_rows(const DropPlan& p, const DropArgs& a, bool bwd, cudaStream_t st) {
+  const dim3 grid((unsigned)p.gx, (unsigned)p.slices), block((unsigned)(p.TX * p.TY));
   if (bwd)
-    return launch(dropout_rows_kernel<T, true, false>, grid, block,
+    return launch(dropout_rows_kernel<T, true, false, STATE>, grid, block,
                   a.part ? sizeof(DF) * 8 * (size_t)(p.TX * p.TY) : 0, st, false, a);
   if (a.res != nullptr)
-    return launch(dropout_rows_kernel<T, false, true>, grid, block, 0, st, false, a);
-  return launch(dropout_rows_kernel<T, false, false>, grid, block, 0, st, false, a);
+    return launch(dropout_rows_kernel<T, false, true, STATE>, grid, block, 0, st, false, a);
+  return launch(dropout_rows_kernel<T, false, false, STATE>, grid, block, 0, st, false, a);
+}
+template <typename T>
+cudaError_t launch_drop(const DropPlan& p, const DropArgs& a, bool bwd, cudaStream_t st) {
+  if (p.fast)
+    return a.rng.state != nullptr ? launch_rows<T, true>(p, a, bwd, st)
+                                  : launch_rows<T, false>(p, a, bwd, st);
+  const dim3 grid((unsigned)p.gx, (unsigned)p.slices);
+  return bwd ? launch(dropout_tile_kernel<T, true>, grid, dim3(kDThreads), 0, st, false, a)
+             : launch(dropout_tile_kernel<T, false>, grid, dim3(kDThreads), 0, st, false, a);
 }
 
 }  // namespace
 
 RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state) {
   RngArgs r;
-  r.seed = seed;
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+  for (int i = 0; i < 10; ++i) {
+    r.key[2 * i] = k0;
+    r.key[2 * i + 1] = k1;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
   r.offset = offset;
   r.state = state;
-  const double k = (1.0 - p) * 65536.0 + 0.5;  // 0.5 .. 65536.5
-  r.thr = (uint32_t)k;
-  r.scale = r.thr ? (float)(65536.0 / (double)r.thr) : 0.f;
+  const uint32_t thr = (uint32_t)((1.0 - p) * 65536.0 + 0.5);  // 0 .. 65536
+  r.all = thr == 65536 ? 1u : 0u;
+  r.lim = thr << 16;
+  r.scale = thr ? (float)(65536.0 / (double)thr) : 0.f;
   return r;
 }
 

@@ -29,10 +29,12 @@
 // are fixed trees, so results are bit-deterministic.
 //
 // The fused form also runs with the counter-based mask of philox.cuh
-// (kRowLnRng): the same kernels, the mask bytes replaced by the generator's
-// bits, and a dropped element contributing exactly 0 whatever it holds.
+// (kRowLnRng), a dropped element contributing exactly 0 whatever it holds:
+// row_fwd_rng_kernel for rows of at most 256 vectors, else the kernels above
+// with the mask bytes replaced by the generator's bits.
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
+#include "packed.cuh"
 #include "philox.cuh"
 
 namespace gbn {
@@ -113,8 +115,8 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
   const T* w = static_cast<const T*>(a.w);
   const T* beta = static_cast<const T*>(a.beta);
   const float invH = 1.f / (float)a.H;
-  Philox gen{};
-  if constexpr (RNG) gen = philox_load(a.rng);
+  PhiloxAny gen;
+  if constexpr (RNG) gen.load(a.rng);
 
   for (int64_t r = team; r < a.R; r += nteams) {
     const int64_t ro = r * (int64_t)a.H;
@@ -149,11 +151,11 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
             for (int e = 0; e < VE; ++e) bv[e] = 0.f;
           }
           if constexpr (RNG) {
-            float f[VE];
-            keep_factors<VE>(gen, (uint64_t)(ro + (int64_t)vi * VE), a.rng.thr, a.scale, f);
+            bool f[VE];
+            gen.g.template keep<VE>(a.rng, (uint64_t)(ro + (int64_t)vi * VE), f);
 #pragma unroll
             for (int e = 0; e < VE; ++e)
-              z[k][e] = fmaf(f[e] != 0.f ? z[k][e] + bv[e] : 0.f, f[e], rv[e]);
+              z[k][e] = fmaf(f[e] ? z[k][e] + bv[e] : 0.f, a.scale, rv[e]);
           } else {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
 template <typename T, int KIND, int UNR>
 __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
   constexpr int VE = 16 / sizeof(T);
-  constexpr bool FUSED = kFusedKind<KIND>, RNG = KIND == kRowLnRng;
+  constexpr bool FUSED = KIND == GBN_ROW_LN_FUSED;
   using V = Vec<T, VE>;
   extern __shared__ __align__(16) float zsm[];
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5;
@@ -260,34 +262,23 @@ __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
   const T* w = static_cast<const T*>(a.w);
   const T* beta = static_cast<const T*>(a.beta);
   const float invH = 1.f / (float)a.H;
-  Philox gen{};
-  if constexpr (RNG) gen = philox_load(a.rng);
-
   auto zvec = [&](int64_t ro, int vi, float (&z)[VE]) {
     V::cvt(V::ld(x + ro + (int64_t)vi * VE), z);
     if constexpr (FUSED) {
       float rv[VE], bv[VE];
       V::cvt(V::ld(res + ro + (int64_t)vi * VE), rv);
-      uint2 mk = make_uint2(0x01010101u, 0x01010101u);
-      if (!RNG && a.mask) mk = load_mask<VE>(a.mask + ro + (int64_t)vi * VE);
+      const uint2 mk = a.mask ? load_mask<VE>(a.mask + ro + (int64_t)vi * VE)
+                              : make_uint2(0x01010101u, 0x01010101u);
       if (bias) {
         V::cvt(V::ld(bias + (int64_t)vi * VE), bv);
       } else {
 #pragma unroll
         for (int e = 0; e < VE; ++e) bv[e] = 0.f;
       }
-      if constexpr (RNG) {
-        float f[VE];
-        keep_factors<VE>(gen, (uint64_t)(ro + (int64_t)vi * VE), a.rng.thr, a.scale, f);
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-          z[e] = fmaf(f[e] != 0.f ? z[e] + bv[e] : 0.f, f[e], rv[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const float keep = mask_byte(mk, e) ? a.scale : 0.f;
-          z[e] = fmaf(keep, z[e] + bv[e], rv[e]);
-        }
+      for (int e = 0; e < VE; ++e) {
+        const float keep = mask_byte(mk, e) ? a.scale : 0.f;
+        z[e] = fmaf(keep, z[e] + bv[e], rv[e]);
       }
     }
   };
@@ -373,6 +364,109 @@ __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
   }
 }
 
+// The drawn mask, rows of at most 256 vectors: one warp per row, the row in
+// registers as packed fp32 pairs (KV vectors a lane: lane, lane + 32, ...).
+// All loads of a row are issued first; z goes out as soon as it is formed, and
+// the registers then hold z - shift for both statistics passes and y.  Bound:
+// instruction issue (the generator is a quarter of ~25 an element), then DRAM.
+template <typename T, int KV, bool STATE>
+__global__ void __launch_bounds__(128, KV > 4 ? 4 : 6) row_fwd_rng_kernel(const FwdArgs a) {
+  constexpr int VE = 16 / sizeof(T);
+  constexpr int NP = VE / 2;
+  using V = Vec<T, VE>;
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r >= a.R) return;
+  const int64_t ro = r * (int64_t)a.H + lane * VE;
+  const bool tail = lane + 32 * (KV - 1) < a.Hv;  // the last vector is this lane's too
+  const T* x = static_cast<const T*>(a.x) + ro;
+  const T* res = static_cast<const T*>(a.res) + ro;
+  typename V::raw rx[KV], rr[KV];
+#pragma unroll
+  for (int k = 0; k < KV; ++k) {
+    rx[k] = rr[k] = typename V::raw{};
+    if (k < KV - 1 || tail) {
+      rx[k] = V::ld(x + k * 32 * VE);
+      rr[k] = V::ld(res + k * 32 * VE);
+    }
+  }
+  Philox<STATE> gen;
+  gen.load(a.rng);
+  const T* bias = static_cast<const T*>(a.bias) + lane * VE;
+  const f2 scale2 = f2_splat(a.scale);
+  f2 z[KV][NP];
+#pragma unroll
+  for (int k = 0; k < KV; ++k) {
+    bool f[VE];
+    gen.template keep<VE>(a.rng, (uint64_t)(ro + k * 32 * VE), f);
+    f2 xv[NP];
+    to_pairs<T, VE>(rx[k], xv);
+    to_pairs<T, VE>(rr[k], z[k]);
+    if (a.bias != nullptr && (k < KV - 1 || tail)) {
+      f2 bv[NP];
+      to_pairs<T, VE>(V::ld(bias + k * 32 * VE), bv);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) xv[p] = f2_add(xv[p], bv[p]);
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const float2 t = f2_unpack(xv[p]);
+      z[k][p] = f2_fma(f2_pack(f[2 * p] ? t.x : 0.f, f[2 * p + 1] ? t.y : 0.f), scale2, z[k][p]);
+    }
+    if (a.z != nullptr && (k < KV - 1 || tail))
+      store_pairs<T, VE>(static_cast<T*>(a.z) + ro + k * 32 * VE, z[k]);
+  }
+  const float shift = __shfl_sync(0xffffffffu, f2_unpack(z[0][0]).x, 0);
+  const f2 nshift2 = f2_splat(-shift);
+  f2 s = 0ull;
+#pragma unroll
+  for (int k = 0; k < KV; ++k)
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      z[k][p] = f2_add(z[k][p], nshift2);
+      if (k == KV - 1 && !tail) z[k][p] = 0ull;
+      s = f2_add(s, z[k][p]);
+    }
+  const float invH = 1.f / (float)a.H;
+  const float md = warp_sum(f2_hsum(s)) * invH;
+  const f2 nmd2 = f2_splat(-md);
+  f2 q = 0ull;
+#pragma unroll
+  for (int k = 0; k < KV; ++k)
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const f2 c = f2_add(z[k][p], nmd2);
+      if (k < KV - 1 || tail) q = f2_fma(c, c, q);
+    }
+  const float rs = 1.f / sqrtf(warp_sum(f2_hsum(q)) * invH + a.eps);
+  const f2 rs2 = f2_splat(rs);
+#pragma unroll
+  for (int k = 0; k < KV; ++k) {
+    if (k == KV - 1 && !tail) break;
+    const int64_t j = (int64_t)(lane + 32 * k) * VE;
+    f2 o[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) o[p] = f2_mul(f2_add(z[k][p], nmd2), rs2);
+    if (a.w != nullptr) {
+      f2 g[NP];
+      to_pairs<T, VE>(V::ld(static_cast<const T*>(a.w) + j), g);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) o[p] = f2_mul(o[p], g[p]);
+    }
+    if (a.beta != nullptr) {
+      f2 b[NP];
+      to_pairs<T, VE>(V::ld(static_cast<const T*>(a.beta) + j), b);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) o[p] = f2_add(o[p], b[p]);
+    }
+    store_pairs<T, VE>(static_cast<T*>(a.y) + ro + k * 32 * VE, o);
+  }
+  if (lane == 0) {
+    a.mean[r] = shift + md;
+    a.rstd[r] = rs;
+  }
+}
+
 // Any H and alignment: block g owns rows g, g+G, ...; each pass walks the
 // row with stride blockDim (z is recomputed, the row is re-read from L2).
 template <typename T, int KIND>
@@ -388,12 +482,12 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   const float invH = 1.f / (float)a.H;
   extern __shared__ __align__(16) uint8_t gbits[];
   RowBits rb{a.H <= kRowBitsMaxH ? gbits : nullptr, 0};
-  Philox gen{};
-  if constexpr (RNG) gen = philox_load(a.rng);
+  PhiloxAny gen;
+  if constexpr (RNG) gen.load(a.rng);
   auto zval = [&](int64_t o, int64_t j) {
     float v = to_f32(x[o + j]);
     if constexpr (RNG) {
-      const bool keep = rowbits_keep(rb, gen, a.rng.thr, (uint64_t)(o + j));
+      const bool keep = rowbits_keep(rb, gen, a.rng, (uint64_t)(o + j));
       v = fmaf(keep ? v + (bias ? to_f32(bias[j]) : 0.f) : 0.f, a.scale, to_f32(res[o + j]));
     } else if constexpr (FUSED) {
       const float keep = (a.mask == nullptr || a.mask[o + j] != 0) ? a.scale : 0.f;
@@ -403,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   };
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
     const int64_t o = r * H;
-    if constexpr (RNG) rowbits_fill(rb, gen, a.rng.thr, (uint64_t)o, H);
+    if constexpr (RNG) rowbits_fill(rb, gen, a.rng, (uint64_t)o, H);
     const float shift = KIND == GBN_ROW_RMS ? 0.f : zval(o, 0);
     float s = 0.f;
     for (int64_t j = threadIdx.x; j < H; j += blockDim.x) {
@@ -438,10 +532,23 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   }
 }
 
+// Row kernels of at most 256 vectors with the drawn mask: KV = vectors a lane.
+template <typename T, int KV>
+cudaError_t launch_rng(const FwdArgs& a, cudaStream_t st) {
+  if constexpr (KV > 1)
+    if (a.Hv <= 32 * (KV - 1)) return launch_rng<T, KV - 1>(a, st);
+  const dim3 grid((unsigned)((a.R + 3) / 4)), block(128);
+  return a.rng.state != nullptr
+             ? launch(row_fwd_rng_kernel<T, KV, true>, grid, block, 0, st, false, a)
+             : launch(row_fwd_rng_kernel<T, KV, false>, grid, block, 0, st, false, a);
+}
+
 template <typename T, int KIND>
 cudaError_t launch_kind(const FwdArgs& a, bool vec_ok, const DevInfo& dev, cudaStream_t st) {
   const int64_t R = a.R;
-  if (vec_ok && a.Hv <= 256) {
+  if constexpr (KIND == kRowLnRng) {
+    if (vec_ok && a.Hv <= 256 && R <= ((int64_t)1 << 32)) return launch_rng<T, 8>(a, st);
+  } else if (vec_ok && a.Hv <= 256) {
     // one warp per row, 8 per block; z of each row in shared memory
     constexpr int VE = 16 / sizeof(T);
     const size_t smem = (size_t)(kThreads / 32) * a.Hv * VE * sizeof(float);
@@ -482,9 +589,6 @@ cudaError_t configure_unr(int bytes) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
     e = r;
   if ((r = cudaFuncSetAttribute(row_fwd_warp_kernel<T, GBN_ROW_LN_FUSED, UNR>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
-    e = r;
-  if ((r = cudaFuncSetAttribute(row_fwd_warp_kernel<T, kRowLnRng, UNR>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
     e = r;
   return e;

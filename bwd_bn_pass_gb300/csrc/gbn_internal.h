@@ -336,8 +336,7 @@ struct RopePlan {
   int vec = 1;        // elements per vector
   int ns = 1;         // slots (pairs of vectors) per lane
   int L = 1;          // lanes per team
-  int hc = 1;         // forward: heads per chunk
-  int cq = 0, ck = 0; // backward: chunks of query / key heads
+  int cq = 0, ck = 0; // chunks of query / key heads
   int64_t bx = 1;     // backward: blocks per chunk
   size_t ws_bytes = 0;
 };
@@ -357,7 +356,7 @@ struct RopePtrs {
   int64_t xt = 0, xh = 0, yt = 0, yh = 0, dt = 0, dh = 0;  // token / head strides
 };
 bool rope_plan(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, bool inter, int dtype,
-               int vec_max, const DevInfo& dev, RopePlan* p);
+               int vec_max, int dir, const DevInfo& dev, RopePlan* p);
 size_t rope_ws_bound(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, int dtype,
                      const DevInfo& dev);
 // dir: 0 forward, 1 backward (without wq: the rotation back of dy).

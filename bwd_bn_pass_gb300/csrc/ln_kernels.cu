@@ -84,7 +84,8 @@ struct LnArgs {
 // Where the fused kernels' keep decisions come from: mask bytes (or none:
 // everything kept), or the generator.
 constexpr int kMaskBytes = 0;
-constexpr int kMaskRng = 1;
+constexpr int kMaskRng = 1;       // round keys from the launch's arguments
+constexpr int kMaskRngState = 2;  // seed and offset from device memory
 
 // One element's LayerNorm input z from the stage (fused: residual +
 // keep*(input + bias), exact (hi, lo) for fp32 outputs).
@@ -152,22 +153,15 @@ __device__ __forceinline__ void keep_pairs(uint2 m, float s, f2 (&keep2)[NP]) {
 
 // All-ones words where the generator keeps the element, else zero, for the NP
 // pairs of the 16-byte vector at element i.
-template <int NP>
-__device__ __forceinline__ void rng_pairs(const Philox& g, uint64_t i, uint32_t thr,
+template <int NP, bool STATE>
+__device__ __forceinline__ void rng_pairs(const Philox<STATE>& g, const RngArgs& a, uint64_t i,
                                           f2 (&keep2)[NP]) {
-  const uint4 w = philox_block(g, i >> 3);
-  uint32_t v[NP];
-  if constexpr (NP == 4) {
-    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-  } else {
-    const bool second = (i & 4) != 0;
-    v[0] = second ? w.z : w.x;
-    v[1] = second ? w.w : w.y;
-  }
+  bool f[2 * NP];
+  g.template keep<2 * NP>(a, i, f);
 #pragma unroll
   for (int p = 0; p < NP; ++p)
-    keep2[p] = f2_pack(__uint_as_float(keep_lo(v[p], thr) ? 0xffffffffu : 0u),
-                       __uint_as_float(keep_hi(v[p], thr) ? 0xffffffffu : 0u));
+    keep2[p] = f2_pack(__uint_as_float(f[2 * p] ? 0xffffffffu : 0u),
+                       __uint_as_float(f[2 * p + 1] ? 0xffffffffu : 0u));
 }
 
 // Warp sums of four values at once (a transposed butterfly: 6 shuffles
@@ -197,8 +191,8 @@ constexpr int kLnRingWarps[3] = {0, kLnRingWarpsKV1, kLnRingWarpsKVn};
 // (two for one-vector rows, else one).  MAXW: consumer warps at most (the
 // register budget of a thread follows from it).
 template <typename T, int KV, bool FUSED, int MASK, int MAXW>
-__global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs a) {
-  constexpr bool RNG = MASK == kMaskRng;
+__global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const LnArgs a) {
+  constexpr bool RNG = MASK != kMaskBytes;
   constexpr int VE = 16 / sizeof(T);
   constexpr bool COMP = sizeof(T) == 4;
   using PK = Pairs16<T>;
@@ -255,8 +249,8 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
     const int ct = tid - 32, lane = ct & 31, cw = ct >> 5;
     const int grp = cw / TPRW, wis = cw - grp * TPRW, lr = ct - grp * TPR;
     epoch_read(sh, a.sync, ct);
-    Philox gen{};
-    if constexpr (RNG) gen = philox_load(a.rng);
+    Philox<MASK == kMaskRngState> gen;
+    if constexpr (RNG) gen.load(a.rng);
     const f2 scale2 = f2_splat(a.scale);
     const int gbar = 2 + grp;  // the group's named barrier
 
@@ -302,7 +296,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
         f2 r2[NP];
         PK::get(rres, r2);
         if constexpr (RNG) {
-          rng_pairs<NP>(gen, i0, a.rng.thr, keep2);
+          rng_pairs<NP>(gen, a.rng, i0, keep2);
 #pragma unroll
           for (int p = 0; p < NP; ++p)
             z2[p] = a.zin ? x2[p]
@@ -339,10 +333,12 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
         float rv[VE];
         Vec<T, VE>::cvt(rres, rv);
         if constexpr (RNG) {
-          keep_factors<VE>(gen, i0, a.rng.thr, a.scale, keep);
+          bool f[VE];
+          gen.template keep<VE>(a.rng, i0, f);
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
-            const bool on = keep[e] != 0.f;
+            const bool on = f[e];
+            keep[e] = on ? a.scale : 0.f;
             z[e] = a.zin ? DF{xv[e], 0.f}
                          : ln_z<FUSED, COMP>(on ? xv[e] : 0.f, rv[e], on ? bia[k][e] : 0.f, keep[e]);
           }
@@ -676,11 +672,11 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(LnArgs 
 // t, t+256, ...; column sums go straight into this block's partial rows.
 template <typename T, bool FUSED, int MASK>
 __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
-  constexpr bool RNG = MASK == kMaskRng;
+  constexpr bool RNG = MASK != kMaskBytes;
   extern __shared__ __align__(16) uint8_t gbits[];
   RowBits rb{a.H <= kRowBitsMaxH ? gbits : nullptr, 0};
-  Philox gen{};
-  if constexpr (RNG) gen = philox_load(a.rng);
+  PhiloxAny gen;
+  if constexpr (RNG) gen.load(a.rng);
   constexpr bool COMP = sizeof(T) == 4;
   __shared__ float red[2][2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
@@ -705,7 +701,7 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
     keep = 1.f;
     if constexpr (FUSED) {
       if constexpr (RNG)
-        keep = rowbits_keep(rb, gen, a.rng.thr, (uint64_t)(r * H + j)) ? a.scale : 0.f;
+        keep = rowbits_keep(rb, gen, a.rng, (uint64_t)(r * H + j)) ? a.scale : 0.f;
       else
         keep = (a.mask == nullptr || a.mask[r * H + j] != 0) ? a.scale : 0.f;
       if (a.zin) return z;
@@ -734,7 +730,7 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
   int it = 0;
   for (int64_t r = g; r < a.R; r += G, ++it) {
     const float mu = a.mean[r], rho = a.rstd[r];
-    if constexpr (RNG) rowbits_fill(rb, gen, a.rng.thr, (uint64_t)(r * H), H);
+    if constexpr (RNG) rowbits_fill(rb, gen, a.rng, (uint64_t)(r * H), H);
     float sg = 0.f, sgx = 0.f;
     for (int64_t j = tid; j < H; j += blockDim.x) {
       float keep;
@@ -815,9 +811,11 @@ cudaError_t launch_ring(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
 // (at most 8), the counts the plan uses.
 template <typename T, bool FUSED, int MASK = kMaskBytes>
 cudaError_t launch_typed(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
-  if (!p.fast)
-    return launch(ln_bwd_generic_kernel<T, FUSED, MASK>, dim3(p.G), dim3(p.threads),
-                  MASK == kMaskRng ? rowbits_bytes(a.H) : 0, st, false, a);
+  if (!p.fast) {
+    constexpr int M = MASK == kMaskBytes ? kMaskBytes : kMaskRng;  // any seed
+    return launch(ln_bwd_generic_kernel<T, FUSED, M>, dim3(p.G), dim3(p.threads),
+                  M == kMaskRng ? rowbits_bytes(a.H) : 0, st, false, a);
+  }
   if constexpr (sizeof(T) == 2)
     if (p.kv == 2) return launch_ring<T, 2, FUSED, MASK>(p, a, st);
   return launch_ring<T, 1, FUSED, MASK>(p, a, st);
@@ -831,7 +829,12 @@ cudaError_t set_smem(int bytes) {
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   cudaError_t e3 = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, true, kMaskRng, kLnRingWarps[KV]>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : e3);
+  cudaError_t e4 =
+      cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, true, kMaskRngState, kLnRingWarps[KV]>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  for (cudaError_t e : {e1, e2, e3, e4})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
 }
 
 template <typename T>
@@ -896,8 +899,12 @@ cudaError_t ln_launch(const RowPlan& p, const LnPtrs& q, void* ws, int* status,
   if (q.rng != nullptr) {
     a.rng = *q.rng;
     a.scale = q.rng->scale;
-    e = p.dtype == GBN_F32 ? launch_typed<float, true, kMaskRng>(p, a, st)
-                           : launch_typed<bf16, true, kMaskRng>(p, a, st);
+    if (a.rng.state != nullptr)
+      e = p.dtype == GBN_F32 ? launch_typed<float, true, kMaskRngState>(p, a, st)
+                             : launch_typed<bf16, true, kMaskRngState>(p, a, st);
+    else
+      e = p.dtype == GBN_F32 ? launch_typed<float, true, kMaskRng>(p, a, st)
+                             : launch_typed<bf16, true, kMaskRng>(p, a, st);
   } else if (p.dtype == GBN_F32)
     e = fused ? launch_typed<float, true>(p, a, st) : launch_typed<float, false>(p, a, st);
   else

@@ -12,9 +12,8 @@
 //
 // Angles: f_i comes as a fraction of a turn in 0.64 fixed point, so
 // pos*f_i modulo 2^64 is the exact angle modulo one turn for every 64-bit
-// position, with two integer multiplies and no double-precision arithmetic;
-// its top bits then go through sincospif (2^-25 of a turn's half is the
-// rounding of the angle, near or far).
+// position, with two integer multiplies and no double-precision arithmetic
+// (2^-25 of half a turn is the rounding of the angle, near or far).
 //
 // Bound: DRAM traffic (forward 2, backward 3 tensors); decoding: latency.
 //
@@ -26,6 +25,7 @@
 // sums are shuffled.
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
+#include "packed.cuh"
 
 namespace gbn {
 
@@ -47,26 +47,34 @@ struct RopeArgs {
   int64_t xt, xh, yt, yh, dt, dh;  // token and head strides of x, out, dy
   int32_t H, HQ, D, rot;
   int32_t L;             // lanes per team
-  int32_t hc;            // heads per chunk (forward)
-  int32_t cq, ck;        // backward: chunks of query and of key heads
+  int32_t cq, ck;        // chunks of query and of key heads
   int32_t pos64;
   float eps, scale;
 };
 
-// cos and sin (times scale) of pos * f turns.
+// cos and sin (times scale) of pos * f turns.  fp32 storage: sincospif.  bf16
+// storage (FAST): the hardware sine and cosine, whose absolute error on
+// [-pi, pi] is 2^-20.5, far below bf16's 2^-9, at a sixth of the instructions.
+template <bool FAST>
 __device__ __forceinline__ void rope_angle(uint64_t pos, uint64_t f, float scale, float& c,
                                            float& s) {
-  const int32_t top = (int32_t)((pos * f) >> 32);  // in [-1/2, 1/2) turns
+  const float top = (float)(int32_t)((pos * f) >> 32);  // 2^-32 turns, in [-1/2, 1/2) turns
   float sn, cs;
-  sincospif((float)top * (1.f / 2147483648.f), &sn, &cs);
+  if constexpr (FAST) __sincosf(top * (3.14159265358979f / 2147483648.f), &sn, &cs);
+  else sincospif(top * (1.f / 2147483648.f), &sn, &cs);
   c = cs * scale;
   s = sn * scale;
 }
 
 template <int VEC, int NS, bool INTER> struct Slots {
+  static constexpr int NP = kPairs<VEC>;
+  // Interleaved pairs lie inside a vector: their rotation is scalar.  Otherwise
+  // element j of the first vector pairs with element j of the second, and two
+  // neighbouring rotations go in one packed instruction.
+  static constexpr bool INSIDE = INTER && VEC > 1;
   int ia[NS], ib[NS];       // first element of the two vectors
   bool va[NS], vb[NS];
-  float cs[NS][VEC], sn[NS][VEC];
+  f2 cs[NS][NP], sn[NS][NP];
   uint32_t turn[NS];        // bit j: pair j of the slot turns
 
   __device__ __forceinline__ void place(const RopeArgs& a, int l) {
@@ -92,42 +100,81 @@ template <int VEC, int NS, bool INTER> struct Slots {
         if (p * VEC + j < half) turn[s] |= 1u << j;
     }
   }
+  template <bool BACK, bool FAST>
   __device__ __forceinline__ void angles(const RopeArgs& a, int l, uint64_t pos) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int s = 0; s < NS; ++s) {
+      float c[VEC], w[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        cs[s][j] = 1.f;
-        sn[s][j] = 0.f;
+        c[j] = 1.f;
+        w[j] = 0.f;
         if ((turn[s] >> j) & 1u)
-          rope_angle(pos, a.freqs[(l + s * a.L) * VEC + j], a.scale, cs[s][j], sn[s][j]);
+          rope_angle<FAST>(pos, a.freqs[(l + s * a.L) * VEC + j], a.scale, c[j], w[j]);
+        if (BACK) w[j] = -w[j];
       }
-  }
-  // (a, b) <- R (a, b), or its transpose (BACK)
-  template <bool BACK>
-  __device__ __forceinline__ void rotate(int s, float (&u)[VEC], float (&v)[VEC]) const {
-    if constexpr (INTER && VEC > 1) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float& p = j < VEC / 2 ? u[2 * j] : v[2 * j - VEC];
-        float& q = j < VEC / 2 ? u[2 * j + 1] : v[2 * j + 1 - VEC];
-        turn_pair<BACK>(s, j, p, q);
+      for (int k = 0; k < NP; ++k) {
+        cs[s][k] = pair_at(c, k);
+        sn[s][k] = pair_at(w, k);
+      }
+    }
+  }
+  // (a, b) <- R (a, b) (its transpose where the angles were made for BACK)
+  __device__ __forceinline__ void rotate(int s, f2 (&u)[NP], f2 (&v)[NP]) const {
+    constexpr uint32_t ALL = (1u << VEC) - 1u;
+    if (turn[s] == ALL) {
+      turn_slot<false>(s, u, v);
+    } else if (turn[s] != 0) {  // the border of the turning part lies inside the slot
+      turn_slot<true>(s, u, v);
+    }
+  }
+  // SELECT: a passing element keeps its bits (it never meets its neighbour)
+  template <bool SELECT>
+  __device__ __forceinline__ void turn_slot(int s, f2 (&u)[NP], f2 (&v)[NP]) const {
+    if constexpr (INSIDE) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {  // pair j: element pair j of u, then of v
+        f2& e = j < VEC / 2 ? u[j < VEC / 2 ? j : 0] : v[j < VEC / 2 ? 0 : j - VEC / 2];
+        const float2 t = f2_unpack(e);
+        const float2 c2 = f2_unpack(cs[s][j / 2]), w2 = f2_unpack(sn[s][j / 2]);
+        const float c = (j & 1) ? c2.y : c2.x, w = (j & 1) ? w2.y : w2.x;
+        const f2 n = f2_pack(fmaf(t.x, c, -(t.y * w)), fmaf(t.y, c, t.x * w));
+        if (!SELECT || ((turn[s] >> j) & 1u)) e = n;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) turn_pair<BACK>(s, j, u[j], v[j]);
-    }
-  }
-  template <bool BACK>
-  __device__ __forceinline__ void turn_pair(int s, int j, float& p, float& q) const {
-    const float c = cs[s][j], w = BACK ? -sn[s][j] : sn[s][j];
-    const float np = fmaf(p, c, -(q * w)), nq = fmaf(q, c, p * w);
-    if ((turn[s] >> j) & 1u) {  // a passing element never meets its neighbour
-      p = np;
-      q = nq;
+      for (int k = 0; k < NP; ++k) {
+        f2 p = f2_fma(u[k], cs[s][k], f2_neg(f2_mul(v[k], sn[s][k])));
+        f2 q = f2_fma(v[k], cs[s][k], f2_mul(u[k], sn[s][k]));
+        if constexpr (SELECT) {
+          const f2 m = ((turn[s] >> (2 * k)) & 1u ? 0xffffffffull : 0ull) |
+                       ((turn[s] >> (2 * k + 1)) & 1u ? 0xffffffff00000000ull : 0ull);
+          p = (p & m) | (u[k] & ~m);
+          q = (q & m) | (v[k] & ~m);
+        }
+        u[k] = p;
+        v[k] = q;
+      }
     }
   }
 };
+
+// Heads [h0, h1) of chunk y: the query heads' chunks first, then the keys'.
+struct RopeChunk {
+  bool is_q;
+  int h0, h1;
+};
+__device__ __forceinline__ RopeChunk rope_chunk(const RopeArgs& a, int y) {
+  RopeChunk c;
+  c.is_q = y < a.cq;
+  const int nh = c.is_q ? a.HQ : a.H - a.HQ, nc = c.is_q ? a.cq : a.ck;
+  const int ch = c.is_q ? y : y - a.cq, base = c.is_q ? 0 : a.HQ;
+  const int per = (nh + nc - 1) / nc;
+  c.h0 = base + min(ch * per, nh);
+  c.h1 = base + min(ch * per + per, nh);
+  return c;
+}
 
 __device__ __forceinline__ uint64_t rope_pos(const RopeArgs& a, int64_t t) {
   return a.pos64 ? static_cast<const uint64_t*>(a.pos)[t]
@@ -139,186 +186,210 @@ __device__ __forceinline__ float team_total(float v, int L) {
   return v;
 }
 
-template <typename T, int VEC>
+// FULL: the lanes' vectors tile the row exactly (ok is always true).
+template <typename T, int VEC, bool FULL = false>
 __device__ __forceinline__ void ld_vec(const T* p, bool ok, typename Vec<T, VEC>::raw& r) {
-  if (ok) r = Vec<T, VEC>::ld(p);
+  if (FULL || ok) r = Vec<T, VEC>::ld(p);
   else r = typename Vec<T, VEC>::raw{};
 }
 
 // Forward (and, without a norm, the backward: BACK).  blockIdx.y: head chunk.
-template <typename T, int VEC, int NS, bool INTER, bool NORM, bool BACK>
-__global__ void __launch_bounds__(kRThreads) rope_fwd_kernel(RopeArgs a) {
-  constexpr int UH = VEC * NS >= 8 ? 2 : 4;  // heads in flight
+template <typename T, int VEC, int NS, bool INTER, bool NORM, bool BACK, bool FULL>
+__global__ void __launch_bounds__(kRThreads, 4) rope_fwd_kernel(const RopeArgs a) {
+  constexpr int UH = 2;  // heads in flight
+  constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   const int l = threadIdx.x & (a.L - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kRThreads / a.L) + threadIdx.x / a.L;
-  const bool live = t < a.T;
-  const int h0 = blockIdx.y * a.hc, h1 = min(h0 + a.hc, a.H);
-  const T* x = static_cast<const T*>(a.x) + (live ? t : 0) * a.xt;
-  T* y = static_cast<T*>(a.out) + (live ? t : 0) * a.yt;
+  const int64_t tq = (int64_t)blockIdx.x * (kRThreads / a.L) + threadIdx.x / a.L;
+  const bool live = tq < a.T;
+  const int64_t t = live ? tq : a.T - 1;  // idle teams read the last token
+  const RopeChunk ch = rope_chunk(a, blockIdx.y);
+  const T* x = static_cast<const T*>(a.x) + t * a.xt + (int64_t)ch.h0 * a.xh;
+  T* y = static_cast<T*>(a.out) + t * a.yt + (int64_t)ch.h0 * a.yh;
   Slots<VEC, NS, INTER> sl;
   sl.place(a, l);
-  typename V::raw wa[2][NS], wb[2][NS];  // weights of query and key heads
+  f2 w0[NS][NP], w1[NS][NP];
   if constexpr (NORM) {
+    const T* w = static_cast<const T*>(ch.is_q ? a.wq : a.wk);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const T* w = static_cast<const T*>(k ? a.wk : a.wq);
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        ld_vec<T, VEC>(w + sl.ia[s], w != nullptr && sl.va[s], wa[k][s]);
-        ld_vec<T, VEC>(w + sl.ib[s], w != nullptr && sl.vb[s], wb[k][s]);
-      }
+    for (int s = 0; s < NS; ++s) {
+      typename V::raw r0, r1;
+      ld_vec<T, VEC, FULL>(w + sl.ia[s], sl.va[s], r0);
+      ld_vec<T, VEC, FULL>(w + sl.ib[s], sl.vb[s], r1);
+      to_pairs<T, VEC>(r0, w0[s]);
+      to_pairs<T, VEC>(r1, w1[s]);
     }
   }
-  sl.angles(a, l, live ? rope_pos(a, t) : 0);
   const float inv_D = 1.f / (float)a.D;
-  for (int hb = h0; hb < h1; hb += UH) {
-    typename V::raw ra[UH][NS], rb[UH][NS];
+  const int nh = ch.h1 - ch.h0;
+  float* rp = NORM && a.rstd != nullptr && l == 0 && live ? a.rstd + t * a.H + ch.h0 : nullptr;
+  typename V::raw ra[UH][NS], rb[UH][NS];
+  auto load = [&](const T* p) {
 #pragma unroll
     for (int u = 0; u < UH; ++u)
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const bool ok = live && hb + u < h1;
-        const T* p = x + (int64_t)(hb + u) * a.xh;
-        ld_vec<T, VEC>(p + sl.ia[s], ok && sl.va[s], ra[u][s]);
-        ld_vec<T, VEC>(p + sl.ib[s], ok && sl.vb[s], rb[u][s]);
+        ld_vec<T, VEC, FULL>(p + u * a.xh + sl.ia[s], sl.va[s], ra[u][s]);
+        ld_vec<T, VEC, FULL>(p + u * a.xh + sl.ib[s], sl.vb[s], rb[u][s]);
       }
+  };
+  // an odd chunk's last round reads its last head twice (and drops one)
+  auto round_at = [&](int hb) { return x + (int64_t)max(min(hb, nh - UH), 0) * a.xh; };
+  const bool pairs = nh >= UH;
+  if (pairs) load(x);  // on their way while the sines and cosines are formed
+  sl.template angles<BACK, sizeof(T) == 2>(a, l, rope_pos(a, t));
+  auto finish = [&](int h, f2 (&m)[NS][NP], f2 (&n)[NS][NP], bool write) {
+    f2 r2 = 0ull;
+    if constexpr (NORM) {
+      f2 q = 0ull;
 #pragma unroll
-    for (int u = 0; u < UH; ++u) {
-      const int h = hb + u;
-      float r = 1.f;
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+          q = f2_fma(m[s][k], m[s][k], f2_fma(n[s][k], n[s][k], q));
+      const float r = rsqrtf(fmaf(team_total(f2_hsum(q), a.L), inv_D, a.eps));
+      r2 = f2_splat(r);
+      if (rp != nullptr && write) rp[h] = r;
+    }
+    if (!write) return;
+    T* o = y + (int64_t)h * a.yh;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
       if constexpr (NORM) {
-        float q = 0.f;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          float m[VEC], n[VEC];
-          V::cvt(ra[u][s], m);
-          V::cvt(rb[u][s], n);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) q = fmaf(m[e], m[e], fmaf(n[e], n[e], q));
+        for (int k = 0; k < NP; ++k) {
+          m[s][k] = f2_mul(f2_mul(m[s][k], r2), w0[s][k]);
+          n[s][k] = f2_mul(f2_mul(n[s][k], r2), w1[s][k]);
         }
-        r = 1.f / sqrtf(team_total(q, a.L) * inv_D + a.eps);
       }
-      if (!live || h >= h1) continue;
-      if (NORM && l == 0 && a.rstd != nullptr) a.rstd[t * a.H + h] = r;
-      T* o = y + (int64_t)h * a.yh;
+      sl.rotate(s, m[s], n[s]);
+      if (FULL || sl.va[s]) store_pairs<T, VEC>(o + sl.ia[s], m[s]);
+      if (FULL || sl.vb[s]) store_pairs<T, VEC>(o + sl.ib[s], n[s]);
+    }
+  };
+  if (!pairs) {  // a chunk of one head
+    f2 m[NS][NP], n[NS][NP];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      ld_vec<T, VEC, FULL>(x + sl.ia[s], sl.va[s], ra[0][s]);
+      ld_vec<T, VEC, FULL>(x + sl.ib[s], sl.vb[s], rb[0][s]);
+      to_pairs<T, VEC>(ra[0][s], m[s]);
+      to_pairs<T, VEC>(rb[0][s], n[s]);
+    }
+    finish(0, m, n, live);
+    return;
+  }
+  for (int hb = 0; hb < nh; hb += UH) {
+    f2 m[UH][NS][NP], n[UH][NS][NP];
+#pragma unroll
+    for (int u = 0; u < UH; ++u)
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        float m[VEC], n[VEC];
-        V::cvt(ra[u][s], m);
-        V::cvt(rb[u][s], n);
-        if constexpr (NORM) {
-          float w0[VEC], w1[VEC];
-          V::cvt(h < a.HQ ? wa[0][s] : wa[1][s], w0);
-          V::cvt(h < a.HQ ? wb[0][s] : wb[1][s], w1);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            m[e] = (m[e] * r) * w0[e];
-            n[e] = (n[e] * r) * w1[e];
-          }
-        }
-        sl.template rotate<BACK>(s, m, n);
-        if (sl.va[s]) V::store(o + sl.ia[s], m);
-        if (sl.vb[s]) V::store(o + sl.ib[s], n);
+        to_pairs<T, VEC>(ra[u][s], m[u][s]);
+        to_pairs<T, VEC>(rb[u][s], n[u][s]);
       }
-    }
+    if (hb + UH < nh) load(round_at(hb + UH));
+    const int h0 = min(hb, nh - UH);
+#pragma unroll
+    for (int u = 0; u < UH; ++u) finish(h0 + u, m[u], n[u], live && h0 + u >= hb);
   }
 }
 
 // Backward with the norm.  blockIdx.y: a chunk of query heads (below cq) or of
 // key heads; blocks stride over the tokens.  A block's weight gradient goes to
 // its row of the partials.
-template <typename T, int VEC, int NS, bool INTER>
-__global__ void __launch_bounds__(kRThreads) rope_bwd_kernel(RopeArgs a) {
+template <typename T, int VEC, int NS, bool INTER, bool FULL>
+__global__ void __launch_bounds__(kRThreads, 2) rope_bwd_kernel(const RopeArgs a) {
   constexpr bool COMP = sizeof(T) == 4;
-  constexpr int UH = VEC * NS >= 8 ? 1 : 2;
+  constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   extern __shared__ DF red[];  // [teams][2 * NS * VEC * L]
   const int l = threadIdx.x & (a.L - 1), team = threadIdx.x / a.L, teams = kRThreads / a.L;
-  const bool is_q = (int)blockIdx.y < a.cq;
-  const int nh = is_q ? a.HQ : a.H - a.HQ, nc = is_q ? a.cq : a.ck;
-  const int ch = is_q ? blockIdx.y : blockIdx.y - a.cq;
-  const int hbase = is_q ? 0 : a.HQ;
-  const int h0 = hbase + (int)((int64_t)nh * ch / nc), h1 = hbase + (int)((int64_t)nh * (ch + 1) / nc);
-  const T* w = static_cast<const T*>(is_q ? a.wq : a.wk);
+  const RopeChunk ch = rope_chunk(a, blockIdx.y);
+  const T* w = static_cast<const T*>(ch.is_q ? a.wq : a.wk);
   Slots<VEC, NS, INTER> sl;
   sl.place(a, l);
-  float w0[NS][VEC], w1[NS][VEC];
-  DF acc[NS][2][VEC];
+  f2 w0[NS][NP], w1[NS][NP];
+  DF2 acc[NS][2][NP];  // fp32 storage carries the sums' errors
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     typename V::raw r0, r1;
     ld_vec<T, VEC>(w + sl.ia[s], sl.va[s], r0);
     ld_vec<T, VEC>(w + sl.ib[s], sl.vb[s], r1);
-    V::cvt(r0, w0[s]);
-    V::cvt(r1, w1[s]);
+    to_pairs<T, VEC>(r0, w0[s]);
+    to_pairs<T, VEC>(r1, w1[s]);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[s][0][e] = acc[s][1][e] = DF{0.f, 0.f};
+    for (int k = 0; k < NP; ++k) acc[s][0][k] = acc[s][1][k] = DF2{0ull, 0ull};
   }
   const float inv_D = 1.f / (float)a.D;
+  const int nh = ch.h1 - ch.h0;
   for (int64_t tb = (int64_t)blockIdx.x * teams; tb < a.T; tb += (int64_t)gridDim.x * teams) {
     const int64_t t = tb + team;
     const bool live = t < a.T;
-    const T* x = static_cast<const T*>(a.x) + (live ? t : 0) * a.xt;
-    const T* d = static_cast<const T*>(a.dy) + (live ? t : 0) * a.dt;
-    T* o = static_cast<T*>(a.out) + (live ? t : 0) * a.yt;
-    sl.angles(a, l, live ? rope_pos(a, t) : 0);
-    for (int hb = h0; hb < h1; hb += UH) {
-      typename V::raw xa[UH][NS], xb[UH][NS], da[UH][NS], db[UH][NS];
-      float rs[UH];
+    const int64_t tt = live ? t : a.T - 1;  // idle teams read the last token
+    const T* x = static_cast<const T*>(a.x) + tt * a.xt + (int64_t)ch.h0 * a.xh;
+    const T* d = static_cast<const T*>(a.dy) + tt * a.dt + (int64_t)ch.h0 * a.dh;
+    T* o = static_cast<T*>(a.out) + tt * a.yt + (int64_t)ch.h0 * a.yh;
+    const float* rp = a.rstd + tt * a.H + ch.h0;
+    typename V::raw xa[NS], xb[NS], da[NS], db[NS];
+    float rs = 0.f;
+    auto load = [&](int h) {
+      rs = live ? rp[h] : 0.f;  // 0: an idle team adds nothing
+      const T* p = x + (int64_t)h * a.xh;
+      const T* q = d + (int64_t)h * a.dh;
 #pragma unroll
-      for (int u = 0; u < UH; ++u) {
-        const bool ok = live && hb + u < h1;
-        rs[u] = ok ? a.rstd[t * a.H + hb + u] : 0.f;
+      for (int s = 0; s < NS; ++s) {
+        ld_vec<T, VEC, FULL>(p + sl.ia[s], sl.va[s], xa[s]);
+        ld_vec<T, VEC, FULL>(p + sl.ib[s], sl.vb[s], xb[s]);
+        ld_vec<T, VEC, FULL>(q + sl.ia[s], sl.va[s], da[s]);
+        ld_vec<T, VEC, FULL>(q + sl.ib[s], sl.vb[s], db[s]);
+      }
+    };
+    load(0);  // on their way while the sines and cosines are formed
+    sl.template angles<true, !COMP>(a, l, rope_pos(a, tt));
+    for (int h = 0; h < nh; ++h) {
+      f2 g0[NS][NP], g1[NS][NP], x0[NS][NP], x1[NS][NP];
+      const float r = rs;
+      const f2 r2 = f2_splat(r);
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const T* p = x + (int64_t)(hb + u) * a.xh;
-          const T* q = d + (int64_t)(hb + u) * a.dh;
-          ld_vec<T, VEC>(p + sl.ia[s], ok && sl.va[s], xa[u][s]);
-          ld_vec<T, VEC>(p + sl.ib[s], ok && sl.vb[s], xb[u][s]);
-          ld_vec<T, VEC>(q + sl.ia[s], ok && sl.va[s], da[u][s]);
-          ld_vec<T, VEC>(q + sl.ib[s], ok && sl.vb[s], db[u][s]);
+      for (int s = 0; s < NS; ++s) {
+        to_pairs<T, VEC>(xa[s], x0[s]);
+        to_pairs<T, VEC>(xb[s], x1[s]);
+        to_pairs<T, VEC>(da[s], g0[s]);
+        to_pairs<T, VEC>(db[s], g1[s]);
+      }
+      if (h + 1 < nh) load(h + 1);
+      f2 q = 0ull;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        sl.rotate(s, g0[s], g1[s]);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          x0[s][k] = f2_mul(x0[s][k], r2);
+          x1[s][k] = f2_mul(x1[s][k], r2);
+          const f2 p0 = f2_mul_rounded(g0[s][k], x0[s][k]), p1 = f2_mul_rounded(g1[s][k], x1[s][k]);
+          if constexpr (COMP) {
+            df2_add(acc[s][0][k], p0);
+            df2_add(acc[s][1][k], p1);
+          } else {
+            acc[s][0][k].hi = f2_add(acc[s][0][k].hi, p0);
+            acc[s][1][k].hi = f2_add(acc[s][1][k].hi, p1);
+          }
+          q = f2_fma(p0, w0[s][k], f2_fma(p1, w1[s][k], q));
         }
       }
+      const f2 nm = f2_splat(-team_total(f2_hsum(q), a.L) * inv_D);
+      if (!live) continue;
+      T* ho = o + (int64_t)h * a.yh;
 #pragma unroll
-      for (int u = 0; u < UH; ++u) {
-        float g0[NS][VEC], g1[NS][VEC], x0[NS][VEC], x1[NS][VEC];
-        float q = 0.f;
+      for (int s = 0; s < NS; ++s) {
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          V::cvt(xa[u][s], x0[s]);
-          V::cvt(xb[u][s], x1[s]);
-          V::cvt(da[u][s], g0[s]);
-          V::cvt(db[u][s], g1[s]);
-          sl.template rotate<true>(s, g0[s], g1[s]);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            x0[s][e] *= rs[u];
-            x1[s][e] *= rs[u];
-            const float p0 = g0[s][e] * x0[s][e], p1 = g1[s][e] * x1[s][e];
-            if constexpr (COMP) {
-              df_add(acc[s][0][e], p0);
-              df_add(acc[s][1][e], p1);
-            } else {
-              acc[s][0][e].hi += p0;
-              acc[s][1][e].hi += p1;
-            }
-            q = fmaf(p0, w0[s][e], fmaf(p1, w1[s][e], q));
-          }
+        for (int k = 0; k < NP; ++k) {
+          g0[s][k] = f2_mul(r2, f2_fma(x0[s][k], nm, f2_mul(g0[s][k], w0[s][k])));
+          g1[s][k] = f2_mul(r2, f2_fma(x1[s][k], nm, f2_mul(g1[s][k], w1[s][k])));
         }
-        const float m = team_total(q, a.L) * inv_D;
-        if (!live || hb + u >= h1) continue;
-        T* ho = o + (int64_t)(hb + u) * a.yh;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            g0[s][e] = rs[u] * fmaf(-x0[s][e], m, g0[s][e] * w0[s][e]);
-            g1[s][e] = rs[u] * fmaf(-x1[s][e], m, g1[s][e] * w1[s][e]);
-          }
-          if (sl.va[s]) V::store(ho + sl.ia[s], g0[s]);
-          if (sl.vb[s]) V::store(ho + sl.ib[s], g1[s]);
-        }
+        if (FULL || sl.va[s]) store_pairs<T, VEC>(ho + sl.ia[s], g0[s]);
+        if (FULL || sl.vb[s]) store_pairs<T, VEC>(ho + sl.ib[s], g1[s]);
       }
     }
   }
@@ -327,9 +398,13 @@ __global__ void __launch_bounds__(kRThreads) rope_bwd_kernel(RopeArgs a) {
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      red[((size_t)team * per + (2 * s) * VEC + e) * a.L + l] = acc[s][0][e];
-      red[((size_t)team * per + (2 * s + 1) * VEC + e) * a.L + l] = acc[s][1][e];
+    for (int e = 0; e < VEC; ++e) {  // one store per element and vector
+      const float2 h0 = f2_unpack(acc[s][0][e / 2].hi), l0 = f2_unpack(acc[s][0][e / 2].lo);
+      const float2 h1 = f2_unpack(acc[s][1][e / 2].hi), l1 = f2_unpack(acc[s][1][e / 2].lo);
+      red[((size_t)team * per + (2 * s) * VEC + e) * a.L + l] =
+          (e & 1) ? DF{h0.y, l0.y} : DF{h0.x, l0.x};
+      red[((size_t)team * per + (2 * s + 1) * VEC + e) * a.L + l] =
+          (e & 1) ? DF{h1.y, l1.y} : DF{h1.x, l1.x};
     }
   __syncthreads();
   const int64_t rows = (int64_t)gridDim.x * (a.cq + a.ck);
@@ -384,29 +459,36 @@ __global__ void __launch_bounds__(1024)
 
 // ----------------------------------------------------------------- host --
 
-template <typename T, int VEC, int NS, bool INTER>
+template <typename T, int VEC, int NS, bool INTER, bool FULL>
 cudaError_t rope_run(const RopePlan& p, const RopeArgs& a, int dir, cudaStream_t st) {
   const bool norm = a.wq != nullptr;
   const int teams = kRThreads / p.L;
+  const dim3 block(kRThreads);
   if (dir == 0 || !norm) {
-    const dim3 grid((unsigned)((a.T + teams - 1) / teams), (unsigned)((a.H + a.hc - 1) / a.hc));
+    const dim3 grid((unsigned)((a.T + teams - 1) / teams), (unsigned)(a.cq + a.ck));
     if (dir == 0)
-      return norm ? launch(rope_fwd_kernel<T, VEC, NS, INTER, true, false>, grid, dim3(kRThreads), 0,
+      return norm ? launch(rope_fwd_kernel<T, VEC, NS, INTER, true, false, FULL>, grid, block, 0,
                            st, false, a)
-                  : launch(rope_fwd_kernel<T, VEC, NS, INTER, false, false>, grid, dim3(kRThreads),
-                           0, st, false, a);
-    return launch(rope_fwd_kernel<T, VEC, NS, INTER, false, true>, grid, dim3(kRThreads), 0, st,
-                  false, a);
+                  : launch(rope_fwd_kernel<T, VEC, NS, INTER, false, false, FULL>, grid, block, 0,
+                           st, false, a);
+    return launch(rope_fwd_kernel<T, VEC, NS, INTER, false, true, FULL>, grid, block, 0, st, false,
+                  a);
   }
   const size_t smem = sizeof(DF) * 2 * NS * VEC * kRThreads;
-  return launch(rope_bwd_kernel<T, VEC, NS, INTER>, dim3((unsigned)p.bx, (unsigned)(a.cq + a.ck)),
-                dim3(kRThreads), smem, st, false, a);
+  return launch(rope_bwd_kernel<T, VEC, NS, INTER, FULL>,
+                dim3((unsigned)p.bx, (unsigned)(a.cq + a.ck)), block, smem, st, false, a);
 }
 template <typename T, int VEC, int NS>
 cudaError_t rope_run_layout(const RopePlan& p, const RopeArgs& a, int dir, bool inter,
                             cudaStream_t st) {
-  return inter ? rope_run<T, VEC, NS, true>(p, a, dir, st)
-               : rope_run<T, VEC, NS, false>(p, a, dir, st);
+  // the lanes' vectors tile the row: no predicate on its loads and stores
+  // (the usual powers of two; narrow vectors are not worth more instances)
+  if constexpr (VEC >= 4)
+    if (2 * VEC * NS * p.L == a.D)
+      return inter ? rope_run<T, VEC, NS, true, true>(p, a, dir, st)
+                   : rope_run<T, VEC, NS, false, true>(p, a, dir, st);
+  return inter ? rope_run<T, VEC, NS, true, false>(p, a, dir, st)
+               : rope_run<T, VEC, NS, false, false>(p, a, dir, st);
 }
 template <typename T>
 cudaError_t rope_dispatch(const RopePlan& p, const RopeArgs& a, int dir, bool inter,
@@ -430,9 +512,9 @@ cudaError_t rope_dispatch(const RopePlan& p, const RopeArgs& a, int dir, bool in
 
 // `vec_max`: the widest vector that alignment and strides allow.
 bool rope_plan(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, bool inter, int dtype,
-               int vec_max, const DevInfo& dev, RopePlan* p) {
+               int vec_max, int dir, const DevInfo& dev, RopePlan* p) {
   *p = RopePlan();
-  int v = dtype == GBN_F32 ? 4 : 8;
+  int v = dtype == GBN_F32 || dir == 0 ? 4 : 8;
   while (v > 1 && (v > vec_max || D % v != 0 || (!inter && (rot / 2) % v != 0))) v /= 2;
   p->vec = v;
   const int64_t slots = (D + 2 * v - 1) / (2 * v);
@@ -449,23 +531,29 @@ bool rope_plan(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, bool in
   // more than one slot a lane: the fewest lanes that hold the row
   while (L > 1 && (int64_t)(L / 2) * p->ns >= slots) L /= 2;
   p->L = L;
-  // heads per chunk: as many as leave three quarters of the SMs' threads busy
-  const int64_t want = (int64_t)dev.sms * 1536;
-  int64_t hc = T * H * L / want;
-  if (hc < 1) hc = 1;
-  if (hc > H) hc = H;
-  const int64_t chunks = (H + hc - 1) / hc;
-  p->hc = (int)((H + chunks - 1) / chunks);
-  // backward: chunks of query heads and of key heads apart
+  // Heads per chunk: few enough for several rounds of blocks over the resident
+  // slots (an even finish), many enough that the sines and cosines of a token,
+  // formed once per chunk, cost little.  Chunks of query heads and of key heads
+  // apart.
   const int64_t teams = kRThreads / L;
   const int64_t tb = (T + teams - 1) / teams;
-  const int64_t blocks = (int64_t)dev.sms * 4;
+  const int64_t slots_sm = (int64_t)dev.sms * (dir == 0 ? 4 : 2);
   const int64_t HK = H - HQ;
-  int64_t per = (tb * H + blocks - 1) / blocks;  // heads per chunk
+  int64_t per = tb * H / (slots_sm * (dir == 0 ? 3 : 6));
   if (per < 1) per = 1;
   p->cq = (int)((HQ + per - 1) / per);
   p->ck = (int)((HK + per - 1) / per);
-  const int64_t cap = (2 * blocks + p->cq + p->ck - 1) / (p->cq + p->ck);
+  // no empty chunk: every chunk but the last has ceil(heads / chunks)
+  auto even = [](int64_t heads, int c) {
+    if (c == 0) return 0;
+    const int64_t each = (heads + c - 1) / c;
+    return (int)((heads + each - 1) / each);
+  };
+  p->cq = even(HQ, p->cq);
+  p->ck = even(HK, p->ck);
+  // backward: one round of resident blocks that stride over the tokens (a row
+  // of weight-gradient partials each)
+  const int64_t cap = (slots_sm + p->cq + p->ck - 1) / (p->cq + p->ck);
   p->bx = tb < cap ? tb : cap;
   const size_t rows = (size_t)p->bx * (size_t)(p->cq + p->ck);
   p->ws_bytes = ((dtype == GBN_F32 ? 2 : 1) * rows * (size_t)D * 4 + 255) & ~(size_t)255;
@@ -478,7 +566,7 @@ size_t rope_ws_bound(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, i
   for (int v : {1, 2, 4, 8})
     for (bool inter : {false, true}) {
       RopePlan p;
-      if (rope_plan(T, H, HQ, D, rot, inter, dtype, v, dev, &p) && p.ws_bytes > most)
+      if (rope_plan(T, H, HQ, D, rot, inter, dtype, v, 1, dev, &p) && p.ws_bytes > most)
         most = p.ws_bytes;
     }
   return most;
@@ -510,7 +598,6 @@ cudaError_t rope_launch(const RopePlan& p, const RopePtrs& q, int dir, int dtype
   a.D = (int32_t)D;
   a.rot = (int32_t)rot;
   a.L = p.L;
-  a.hc = p.hc;
   a.cq = p.cq;
   a.ck = p.ck;
   a.eps = eps;
