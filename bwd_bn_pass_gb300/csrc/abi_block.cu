@@ -21,7 +21,7 @@ int rng_check(double p, const uint64_t* state) {
 
 int gn_check(int dtype, int64_t N, int64_t S, int64_t C, int64_t G, int act, float slope) {
   if (dtype != GBN_F32 && dtype != GBN_BF16) return GBN_EDTYPE;
-  if (N < 0 || S < 0 || C < 0 || C > (1 << 30) || N > INT32_MAX || S > (1 << 30))
+  if (N < 0 || S < 0 || C < 0 || C > (1 << 28) || N > INT32_MAX || S > (1 << 30))
     return GBN_EINVAL;
   if (G < 1 || G > INT32_MAX || C % G != 0) return GBN_EINVAL;
   int64_t m, n;
@@ -202,7 +202,9 @@ int gbn_gn_nhwc_forward_train(const void* x, int dtype, int64_t N, int64_t S, in
   if (!dev) return GBN_ECUDA;
   const void* ptrs[2] = {x, y};
   GnPlan p;
-  if (!gn_plan(N, S, C, G, bn_vec_width(dtype, C, ptrs, 2), dtype == GBN_F32 ? 4 : 2, false, *dev, &p)) return GBN_EINVAL;
+  if (!gn_plan(N, S, C, G, bn_vec_width(dtype, C, ptrs, 2), dtype == GBN_F32 ? 4 : 2, false, *dev,
+               &p))
+    return GBN_EINVAL;
   if (ws_bytes < p.ws_bytes) return GBN_EWORKSPACE;
   return to_status(gn_forward(p, dtype, x, gamma, beta, eps, act, slope, y, stats, ws,
                               static_cast<cudaStream_t>(stream)));
@@ -228,7 +230,11 @@ int gbn_gn_nhwc_backward(const void* x, const void* dy, int dtype, int64_t N, in
   }
   const void* ptrs[3] = {x, dy, dx};
   GnPlan p;
-  if (!gn_plan(N, S, C, G, bn_vec_width(dtype, C, ptrs, 3), dtype == GBN_F32 ? 4 : 2, true, *dev, &p)) return GBN_EINVAL;
+  // at most four channels a thread: the sums' registers then leave four blocks
+  // per SM (eight: two), which the latency of two loads and an exponential needs
+  const int width = bn_vec_width(dtype, C, ptrs, 3);
+  if (!gn_plan(N, S, C, G, width < 4 ? width : 4, dtype == GBN_F32 ? 4 : 2, true, *dev, &p))
+    return GBN_EINVAL;
   if (ws_bytes < p.ws_bytes) return GBN_EWORKSPACE;
   return to_status(gn_backward(p, dtype, x, dy, stats, gamma, beta, act, slope, dx, dgamma, dbeta,
                                ws, st));

@@ -18,6 +18,7 @@
 // colsum_kernel (no atomics).
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
+#include "packed.cuh"
 #include "philox.cuh"
 
 namespace gbn {
@@ -37,37 +38,37 @@ struct DropArgs {
   int64_t R;
   int32_t H;
   int32_t Hc;        // chunks per row (rows kernel)
-  int32_t TX, TY;    // rows kernel: chunks x rows of a block
+  int32_t ltx;       // rows kernel: log2 of the block's chunks per row
   int32_t slices;
   RngArgs rng;
 };
 
-// Eight elements of T as two or one 16-byte vectors.
+// Eight elements of T as one or two 16-byte vectors, and as packed pairs.
 template <typename T> struct Chunk8 {
   static constexpr int NV = sizeof(T) / 2;  // 16-byte vectors
   static constexpr int VE = 16 / sizeof(T);
   using V = Vec<T, VE>;
   uint4 raw[NV];
-  __device__ void load(const T* p) {
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) raw[k] = V::ld(p + k * VE);
   }
-  __device__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(f2 (&v)[4]) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float t[VE];
-      V::cvt(raw[k], t);
+      f2 t[VE / 2];
+      to_pairs<T, VE>(raw[k], t);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) v[k * VE + e] = t[e];
+      for (int e = 0; e < VE / 2; ++e) v[k * (VE / 2) + e] = t[e];
     }
   }
-  __device__ static void store(T* p, const float (&v)[8]) {
+  __device__ __forceinline__ static void store(T* p, const f2 (&v)[4]) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float t[VE];
+      f2 t[VE / 2];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) t[e] = v[k * VE + e];
-      V::store(p + k * VE, t);
+      for (int e = 0; e < VE / 2; ++e) t[e] = v[k * (VE / 2) + e];
+      store_pairs<T, VE>(p + k * VE, t);
     }
   }
 };
@@ -86,36 +87,41 @@ template <typename T> struct ColSum {
   }
 };
 
-template <typename T, bool BWD, bool RES, bool STATE>
-__global__ void __launch_bounds__(kDThreads, 4) dropout_rows_kernel(const DropArgs a) {
-  constexpr int U = sizeof(T) == 2 ? (RES ? 2 : 4) : (RES ? 1 : 2);  // rows in flight
+// A block is 2^ltx chunks x 256 / 2^ltx rows.
+template <typename T, bool BWD, bool RES>
+__global__ void __launch_bounds__(kDThreads, 4)
+    dropout_rows_kernel(const DropArgs a) {
+  constexpr bool COMP = sizeof(T) == 4;
+  constexpr int U = RES ? 1 : 2;  // rows in flight (per thread; 32 bytes or more)
   using C8 = Chunk8<T>;
-  extern __shared__ DF red[];  // [TY][TX][8] when sums are asked for
-  const int ty = threadIdx.x / a.TX, tx = threadIdx.x - ty * a.TX;
-  const int cv = blockIdx.x * a.TX + tx;
+  __shared__ DF red[BWD ? kDThreads / 32 : 1][BWD ? 32 * 8 : 1];  // [warp][column of the tile]
+  const int TX = 1 << a.ltx, TY = kDThreads >> a.ltx;
+  const int tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> a.ltx;
+  const int cv = (int)blockIdx.x * TX + tx;
   const bool active = cv < a.Hc;
   const int64_t H = a.H;
   const int64_t r0 = a.R * blockIdx.y / a.slices, r1 = a.R * (blockIdx.y + 1) / a.slices;
-  Philox<STATE> g;
-  g.load(a.rng);
-  const float scale = a.rng.scale;
-  float b[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) b[e] = 0.f;
-  ColSum<T> sum[8];
+  __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  philox_fill(keys, a.rng);
+  __syncthreads();
+  Philox<true> g;
+  g.load(a.rng, keys);
+  const f2 scale2 = f2_splat(a.rng.scale);
+  f2 b[4] = {0ull, 0ull, 0ull, 0ull};
+  DF2 sum[4] = {{0ull, 0ull}, {0ull, 0ull}, {0ull, 0ull}, {0ull, 0ull}};
   if (active) {
     if (!BWD && a.bias != nullptr) {
       C8 c;
       c.load(static_cast<const T*>(a.bias) + (int64_t)cv * 8);
       c.get(b);
     }
-    const int64_t first = r0 + ty, step = (int64_t)a.TY * H;
+    const int64_t first = r0 + ty, step = (int64_t)TY * H;
     const T* x = static_cast<const T*>(a.x) + first * H + (int64_t)cv * 8;
     const T* res = static_cast<const T*>(a.res) + first * H + (int64_t)cv * 8;
     T* y = static_cast<T*>(a.y) + first * H + (int64_t)cv * 8;
     uint64_t blk = (uint64_t)(first * a.Hc + cv);
-    const uint64_t bstep = (uint64_t)a.TY * a.Hc;
-    int64_t left = r1 > first ? (r1 - first + a.TY - 1) / a.TY : 0;
+    const uint64_t bstep = (uint64_t)TY * a.Hc;
+    int64_t left = r1 > first ? (r1 - first + TY - 1) / TY : 0;
     for (; left > 0; left -= U) {
       C8 cx[U], cr[U];
 #pragma unroll
@@ -128,16 +134,20 @@ __global__ void __launch_bounds__(kDThreads, 4) dropout_rows_kernel(const DropAr
       for (int u = 0; u < U; ++u) {
         if (u >= left) continue;
         bool f[8];
-        float v[8], o[8];
-        g.template keep<8>(a.rng, blk << 3, f);
+        f2 v[4], o[4];
+        g.template keep<8>(blk << 3, f);
         cx[u].get(v);
         if constexpr (RES) cr[u].get(o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int p = 0; p < 4; ++p) {
           // a dropped element is exactly 0 (or the residual), whatever x holds
-          const float t = f[e] ? (BWD ? v[e] : v[e] + b[e]) : 0.f;
-          o[e] = RES ? fmaf(t, scale, o[e]) : t * scale;
-          if constexpr (BWD) sum[e].add(o[e]);
+          const float2 t = f2_unpack(BWD ? v[p] : f2_add(v[p], b[p]));
+          const f2 k = f2_pack(f[2 * p] ? t.x : 0.f, f[2 * p + 1] ? t.y : 0.f);
+          o[p] = RES ? f2_fma(k, scale2, o[p]) : f2_mul_rounded(k, scale2);
+          if constexpr (BWD) {
+            if constexpr (COMP) df2_add(sum[p], o[p]);
+            else sum[p].hi = f2_add(sum[p].hi, o[p]);
+          }
         }
         C8::store(y + u * step, o);
         blk += bstep;
@@ -149,22 +159,34 @@ __global__ void __launch_bounds__(kDThreads, 4) dropout_rows_kernel(const DropAr
   }
   if constexpr (BWD) {
     if (a.part == nullptr) return;
-    // the block's rows of threads, added in order
-    if (active)
+    // the warp's rows by a fixed shuffle tree, then the warps in order
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) red[((size_t)ty * a.TX + tx) * 8 + e] = sum[e].s;
-    __syncthreads();
-    if (ty == 0 && active) {
-      for (int q = 1; q < a.TY; ++q)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e].add(red[((size_t)q * a.TX + tx) * 8 + e]);
-      float* hi = a.part + (int64_t)blockIdx.y * H + (int64_t)cv * 8;
-      float* lo = hi + (int64_t)a.slices * H;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        hi[e] = sum[e].s.hi;
-        if constexpr (sizeof(T) == 4) lo[e] = sum[e].s.lo;
+    for (int p = 0; p < 4; ++p) {
+      const float2 h = f2_unpack(sum[p].hi), lw = f2_unpack(sum[p].lo);
+      DF u{h.x, lw.x}, w{h.y, lw.y};
+      for (int o = 16; o >= TX; o >>= 1) {
+        if constexpr (COMP) {
+          u = df_sum(u, shfl_xor_df(u, o));
+          w = df_sum(w, shfl_xor_df(w, o));
+        } else {
+          u.hi += __shfl_xor_sync(0xffffffffu, u.hi, o);
+          w.hi += __shfl_xor_sync(0xffffffffu, w.hi, o);
+        }
       }
+      if (lane < TX) {
+        red[warp][lane * 8 + 2 * p] = u;
+        red[warp][lane * 8 + 2 * p + 1] = w;
+      }
+    }
+    __syncthreads();
+    const int64_t j = (int64_t)blockIdx.x * TX * 8 + threadIdx.x;
+    if (threadIdx.x < TX * 8 && j < H) {
+      ColSum<T> t;
+#pragma unroll
+      for (int q = 0; q < kDThreads / 32; ++q) t.add(red[q][threadIdx.x]);
+      a.part[(int64_t)blockIdx.y * H + j] = t.s.hi;
+      if constexpr (COMP) a.part[((int64_t)a.slices + blockIdx.y) * H + j] = t.s.lo;
     }
     pdl_launch_dependents();
   }
@@ -182,7 +204,7 @@ __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.res);
   T* y = static_cast<T*>(a.y);
-  PhiloxAny g;
+  Philox<false> g;
   g.load(a.rng);
   const float b = !BWD && active && a.bias ? to_f32(static_cast<const T*>(a.bias)[j]) : 0.f;
   ColSum<T> sum;
@@ -199,7 +221,7 @@ __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
       }
     }
     if (r + wr < r1)
-      bits[wr][wl] = (uint8_t)g.bits(a.rng, ((uint64_t)((r + wr) * H + j0) >> 3) + wl);
+      bits[wr][wl] = (uint8_t)g.bits(((uint64_t)((r + wr) * H + j0) >> 3) + wl);
     __syncthreads();
     if (active) {
 #pragma unroll
@@ -226,21 +248,18 @@ __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
   }
 }
 
-template <typename T, bool STATE>
+template <typename T>
 cudaError_t launch_rows(const DropPlan& p, const DropArgs& a, bool bwd, cudaStream_t st) {
-  const dim3 grid((unsigned)p.gx, (unsigned)p.slices), block((unsigned)(p.TX * p.TY));
+  const dim3 grid((unsigned)p.gx, (unsigned)p.slices), block(kDThreads);
   if (bwd)
-    return launch(dropout_rows_kernel<T, true, false, STATE>, grid, block,
-                  a.part ? sizeof(DF) * 8 * (size_t)(p.TX * p.TY) : 0, st, false, a);
+    return launch(dropout_rows_kernel<T, true, false>, grid, block, 0, st, false, a);
   if (a.res != nullptr)
-    return launch(dropout_rows_kernel<T, false, true, STATE>, grid, block, 0, st, false, a);
-  return launch(dropout_rows_kernel<T, false, false, STATE>, grid, block, 0, st, false, a);
+    return launch(dropout_rows_kernel<T, false, true>, grid, block, 0, st, false, a);
+  return launch(dropout_rows_kernel<T, false, false>, grid, block, 0, st, false, a);
 }
 template <typename T>
 cudaError_t launch_drop(const DropPlan& p, const DropArgs& a, bool bwd, cudaStream_t st) {
-  if (p.fast)
-    return a.rng.state != nullptr ? launch_rows<T, true>(p, a, bwd, st)
-                                  : launch_rows<T, false>(p, a, bwd, st);
+  if (p.fast) return launch_rows<T>(p, a, bwd, st);
   const dim3 grid((unsigned)p.gx, (unsigned)p.slices);
   return bwd ? launch(dropout_tile_kernel<T, true>, grid, dim3(kDThreads), 0, st, false, a)
              : launch(dropout_tile_kernel<T, false>, grid, dim3(kDThreads), 0, st, false, a);
@@ -250,13 +269,7 @@ cudaError_t launch_drop(const DropPlan& p, const DropArgs& a, bool bwd, cudaStre
 
 RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state) {
   RngArgs r;
-  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
-  for (int i = 0; i < 10; ++i) {
-    r.key[2 * i] = k0;
-    r.key[2 * i + 1] = k1;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
+  r.seed = seed;
   r.offset = offset;
   r.state = state;
   const uint32_t thr = (uint32_t)((1.0 - p) * 65536.0 + 0.5);  // 0 .. 65536
@@ -269,20 +282,25 @@ RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state
 DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo& dev) {
   DropPlan p;
   p.fast = fast_ok && H % 8 == 0;
-  const int64_t rows_per_round = dtype == GBN_F32 ? 2 : 4;
   int64_t min_rows;
   if (p.fast) {
+    // chunks of a block row: 32, 16 or 8 (at least 128 contiguous bytes),
+    // whichever leaves the fewest idle threads, the widest on a tie; a narrower
+    // row takes the power of two that holds it
     const int64_t Hc = H / 8;
-    p.gx = (Hc + kDThreads - 1) / kDThreads;
-    p.TX = (int)((Hc + p.gx - 1) / p.gx);
-    p.TY = kDThreads / p.TX;
-    min_rows = rows_per_round * p.TY;  // one round of loads a block, at least
+    p.ltx = 5;
+    auto padded = [Hc](int l) { return ((Hc + (1 << l) - 1) >> l) << l; };
+    for (int l = 4; l >= 3; --l)
+      if (padded(l) < padded(p.ltx)) p.ltx = l;
+    while (p.ltx > 0 && Hc <= (1 << (p.ltx - 1))) --p.ltx;
+    p.gx = (Hc + (1 << p.ltx) - 1) >> p.ltx;
+    min_rows = 2 * (kDThreads >> p.ltx);  // two rows a thread, at least
   } else {
     p.gx = (H + kDTileCols - 1) / kDTileCols;
     min_rows = kDTileRows;
   }
   // every resident block slot once
-  int64_t s = ((int64_t)dev.sms * kDBlocksPerSm + p.gx - 1) / p.gx;
+  int64_t s = (int64_t)dev.sms * kDBlocksPerSm / p.gx;
   const int64_t by_rows = (R + min_rows - 1) / min_rows;
   if (s > by_rows) s = by_rows;
   if (s < 1) s = 1;
@@ -295,14 +313,14 @@ DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo&
 cudaError_t drop_forward(const DropPlan& p, int dtype, const void* x, const void* bias,
                          const void* res, void* y, int64_t R, int64_t H, const RngArgs& rng,
                          cudaStream_t st) {
-  DropArgs a{x, res, bias, y, nullptr, R, (int32_t)H, (int32_t)(H / 8), p.TX, p.TY, p.slices, rng};
+  DropArgs a{x, res, bias, y, nullptr, R, (int32_t)H, (int32_t)(H / 8), p.ltx, p.slices, rng};
   return dtype == GBN_F32 ? launch_drop<float>(p, a, false, st) : launch_drop<bf16>(p, a, false, st);
 }
 
 cudaError_t drop_backward(const DropPlan& p, int dtype, const void* dy, void* dx, void* dbias,
                           void* ws, int64_t R, int64_t H, const RngArgs& rng, cudaStream_t st) {
   DropArgs a{dy, nullptr, nullptr, dx, dbias ? static_cast<float*>(ws) : nullptr, R, (int32_t)H,
-             (int32_t)(H / 8), p.TX, p.TY, p.slices, rng};
+             (int32_t)(H / 8), p.ltx, p.slices, rng};
   cudaError_t e =
       dtype == GBN_F32 ? launch_drop<float>(p, a, true, st) : launch_drop<bf16>(p, a, true, st);
   if (e != cudaSuccess || dbias == nullptr) return e;

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
   const T* w = static_cast<const T*>(a.w);
   const T* beta = static_cast<const T*>(a.beta);
   const float invH = 1.f / (float)a.H;
-  PhiloxAny gen;
+  Philox<false> gen;
   if constexpr (RNG) gen.load(a.rng);
 
   for (int64_t r = team; r < a.R; r += nteams) {
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
           }
           if constexpr (RNG) {
             bool f[VE];
-            gen.g.template keep<VE>(a.rng, (uint64_t)(ro + (int64_t)vi * VE), f);
+            gen.template keep<VE>((uint64_t)(ro + (int64_t)vi * VE), f);
 #pragma unroll
             for (int e = 0; e < VE; ++e)
               z[k][e] = fmaf(f[e] ? z[k][e] + bv[e] : 0.f, a.scale, rv[e]);
@@ -369,13 +369,16 @@ __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
 // All loads of a row are issued first; z goes out as soon as it is formed, and
 // the registers then hold z - shift for both statistics passes and y.  Bound:
 // instruction issue (the generator is a quarter of ~25 an element), then DRAM.
-template <typename T, int KV, bool STATE>
+template <typename T, int KV>
 __global__ void __launch_bounds__(128, KV > 4 ? 4 : 6) row_fwd_rng_kernel(const FwdArgs a) {
   constexpr int VE = 16 / sizeof(T);
   constexpr int NP = VE / 2;
   using V = Vec<T, VE>;
   const int lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  philox_fill(keys, a.rng);
+  __syncthreads();
   if (r >= a.R) return;
   const int64_t ro = r * (int64_t)a.H + lane * VE;
   const bool tail = lane + 32 * (KV - 1) < a.Hv;  // the last vector is this lane's too
@@ -390,15 +393,15 @@ __global__ void __launch_bounds__(128, KV > 4 ? 4 : 6) row_fwd_rng_kernel(const 
       rr[k] = V::ld(res + k * 32 * VE);
     }
   }
-  Philox<STATE> gen;
-  gen.load(a.rng);
+  Philox<true> gen;
+  gen.load(a.rng, keys);
   const T* bias = static_cast<const T*>(a.bias) + lane * VE;
   const f2 scale2 = f2_splat(a.scale);
   f2 z[KV][NP];
 #pragma unroll
   for (int k = 0; k < KV; ++k) {
     bool f[VE];
-    gen.template keep<VE>(a.rng, (uint64_t)(ro + k * 32 * VE), f);
+    gen.template keep<VE>((uint64_t)(ro + k * 32 * VE), f);
     f2 xv[NP];
     to_pairs<T, VE>(rx[k], xv);
     to_pairs<T, VE>(rr[k], z[k]);
@@ -482,12 +485,12 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   const float invH = 1.f / (float)a.H;
   extern __shared__ __align__(16) uint8_t gbits[];
   RowBits rb{a.H <= kRowBitsMaxH ? gbits : nullptr, 0};
-  PhiloxAny gen;
+  Philox<false> gen;
   if constexpr (RNG) gen.load(a.rng);
   auto zval = [&](int64_t o, int64_t j) {
     float v = to_f32(x[o + j]);
     if constexpr (RNG) {
-      const bool keep = rowbits_keep(rb, gen, a.rng, (uint64_t)(o + j));
+      const bool keep = rowbits_keep(rb, gen, (uint64_t)(o + j));
       v = fmaf(keep ? v + (bias ? to_f32(bias[j]) : 0.f) : 0.f, a.scale, to_f32(res[o + j]));
     } else if constexpr (FUSED) {
       const float keep = (a.mask == nullptr || a.mask[o + j] != 0) ? a.scale : 0.f;
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   };
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
     const int64_t o = r * H;
-    if constexpr (RNG) rowbits_fill(rb, gen, a.rng, (uint64_t)o, H);
+    if constexpr (RNG) rowbits_fill(rb, gen, (uint64_t)o, H);
     const float shift = KIND == GBN_ROW_RMS ? 0.f : zval(o, 0);
     float s = 0.f;
     for (int64_t j = threadIdx.x; j < H; j += blockDim.x) {
@@ -538,9 +541,7 @@ cudaError_t launch_rng(const FwdArgs& a, cudaStream_t st) {
   if constexpr (KV > 1)
     if (a.Hv <= 32 * (KV - 1)) return launch_rng<T, KV - 1>(a, st);
   const dim3 grid((unsigned)((a.R + 3) / 4)), block(128);
-  return a.rng.state != nullptr
-             ? launch(row_fwd_rng_kernel<T, KV, true>, grid, block, 0, st, false, a)
-             : launch(row_fwd_rng_kernel<T, KV, false>, grid, block, 0, st, false, a);
+  return launch(row_fwd_rng_kernel<T, KV>, grid, block, 0, st, false, a);
 }
 
 template <typename T, int KIND>

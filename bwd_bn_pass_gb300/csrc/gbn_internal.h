@@ -374,7 +374,7 @@ RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state
 struct DropPlan {
   bool fast = false;    // 8-element chunks per thread (else the tile kernel)
   int64_t gx = 1;       // column tiles
-  int TX = 1, TY = 1;   // fast: chunks x rows of a block
+  int ltx = 0;          // fast: log2 of the chunks of a block's row
   int slices = 1;       // row slices (= rows of partial column sums)
   size_t ws_bytes = 0;  // backward with dbias: the partials
 };

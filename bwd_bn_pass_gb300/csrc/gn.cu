@@ -19,21 +19,24 @@
 // most one group).
 //
 // Statistics: a thread forms mean and centred sum of squares of each of its
-// channels over a few rows held in registers (two passes over the registers),
-// and merges such chunks pairwise (Chan, Golub, LeVeque, "Updating formulae and
-// a pairwise algorithm for computing sample variances", 1979): no difference of
-// large squares appears anywhere, whatever the first element is.  Means are
-// kept relative to the sample's first row (x[n, 0, c]), so a large common
-// offset costs nothing.  All combinations run in a fixed order: two runs give
-// the same bits, and there are no atomics.
+// channels over chunks of four rows, relative to the chunk's own first row (so
+// sum d^2 - (sum d)^2/4 loses at most a factor 4 to cancellation, whatever the
+// data), and merges the chunks pairwise (Chan, Golub, LeVeque, "Updating
+// formulae and a pairwise algorithm for computing sample variances", 1979): no
+// difference of large squares appears anywhere.  Means are kept relative to the
+// sample's first row (x[n, 0, c]), so a large common offset costs nothing.  All
+// combinations run in a fixed order: two runs give the same bits, and there are
+// no atomics.
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
+#include "packed.cuh"
 
 namespace gbn {
 
 namespace {
 
 constexpr int kGThreads = 256;
+constexpr int kGnFewRows = 8;  // thread rows that one thread adds up per channel
 
 struct GnGeom {
   int32_t S;          // rows per sample
@@ -45,6 +48,9 @@ struct GnGeom {
   int32_t rps;        // rows per slice (the last may have fewer)
   int32_t E;          // group partials per (sample, slice): G + T - 1
   int32_t n0;         // first sample of this launch
+  int32_t cols, R;    // finalize: groups side by side, thread rows
+  int32_t llc;        // log2 of the lanes over a group's channels
+  FastDiv dTX, dCg, dcols, dTY;
 };
 
 struct GnArgs {
@@ -55,18 +61,22 @@ struct GnArgs {
   const float* beta;    // null: zeros
   float* stats;         // [3][N][G]: mean, rstd, mean's low part
   float2* gpart;        // [N][slices][E]: forward (mean - shift, M2); backward sums
-  float* cpart;         // backward: [2][2][N*slices][C] (dgamma, dbeta; hi, lo);
+  float* cpart;         // backward: [2][N*slices][C] (dgamma, dbeta);
                         // forward: [N][G], the shifts (y may overwrite x's first row)
   GnGeom g;
   float eps, slope;
 };
 
+// Grid: (tile, slice, sample).
 struct GnBlock {
   int n, slice, tile;
   int tx, ty;
   int cv;               // vector of this thread
   bool active;
-  int r0, r1;           // rows of the slice
+  int r0, rows;         // rows of the slice
+  int left;             // rows of this thread: r0 + ty, r0 + ty + TY, ...
+  uint32_t off, step;   // its first row's vector from the slice's start; between its rows
+                        // (elements; a slice spans less than 2^31 bytes)
   int c0, c1;           // channels of the tile
   int g0, g1;           // groups with a channel in the tile
 };
@@ -74,52 +84,26 @@ struct GnBlock {
 template <int VEC>
 __device__ __forceinline__ GnBlock gn_block(const GnGeom& g) {
   GnBlock b;
-  const uint32_t bi = blockIdx.x;
-  const uint32_t q = bi / (uint32_t)g.T;
-  b.tile = bi - q * g.T;
-  const uint32_t n = q / (uint32_t)g.slices;
-  b.slice = q - n * g.slices;
-  b.n = g.n0 + (int)n;
-  b.ty = (uint32_t)threadIdx.x / (uint32_t)g.TX;
+  b.tile = blockIdx.x;
+  b.slice = blockIdx.y;
+  b.n = g.n0 + (int)blockIdx.z;
+  b.ty = fast_div(threadIdx.x, g.dTX);
   b.tx = threadIdx.x - b.ty * g.TX;
   b.cv = b.tile * g.TX + b.tx;
   b.active = b.ty < g.TY && b.cv < g.Cv;
   b.r0 = b.slice * g.rps;
-  b.r1 = min(b.r0 + g.rps, g.S);
+  b.rows = min(g.rps, g.S - b.r0);
+  b.left = b.rows > b.ty ? (int)fast_div(b.rows - b.ty + g.TY - 1, g.dTY) : 0;
+  b.step = (uint32_t)g.TY * (uint32_t)g.C;
+  b.off = (uint32_t)b.ty * (uint32_t)g.C + (uint32_t)b.cv * VEC;
   b.c0 = b.tile * g.TX * VEC;
   b.c1 = min(b.c0 + g.TX * VEC, g.C);
-  b.g0 = b.c0 / g.Cg;
-  b.g1 = (b.c1 - 1) / g.Cg + 1;
+  b.g0 = g.T == 1 ? 0 : (int)fast_div(b.c0, g.dCg);
+  b.g1 = g.T == 1 ? g.G : (int)fast_div(b.c1 - 1, g.dCg) + 1;
   return b;
 }
 
 // ------------------------------------------------------------ activations --
-
-template <int VEC> struct GnP {
-  static constexpr int NP = (VEC + 1) / 2;  // packed pairs; VEC = 1 pads with 0
-};
-template <typename T, int VEC>
-__device__ __forceinline__ void gn_pairs(typename Vec<T, VEC>::raw r, f2 (&p)[GnP<VEC>::NP]) {
-  float v[VEC];
-  Vec<T, VEC>::cvt(r, v);
-#pragma unroll
-  for (int k = 0; k < GnP<VEC>::NP; ++k) p[k] = f2_pack(v[2 * k], 2 * k + 1 < VEC ? v[2 * k + 1] : 0.f);
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void gn_store(T* p, const f2 (&o)[GnP<VEC>::NP]) {
-  float v[VEC];
-#pragma unroll
-  for (int k = 0; k < GnP<VEC>::NP; ++k) {
-    const float2 t = f2_unpack(o[k]);
-    v[2 * k] = t.x;
-    if (2 * k + 1 < VEC) v[2 * k + 1] = t.y;
-  }
-  Vec<T, VEC>::store(p, v);
-}
-template <int VEC>
-__device__ __forceinline__ f2 gn_pair(const float (&v)[VEC], int k) {
-  return f2_pack(v[2 * k], 2 * k + 1 < VEC ? v[2 * k + 1] : 0.f);
-}
 
 __device__ __forceinline__ float ex2_fast(float v) {
   float r;
@@ -132,54 +116,53 @@ __device__ __forceinline__ float rcp_fast(float v) {
   return r;
 }
 
-// Sigmoid of a pair.  fp32 storage: expf and an IEEE division.  bf16 storage:
-// the hardware exponential and reciprocal (a few 2^-22, far below bf16's 2^-9),
-// and one reciprocal for both, 1/a = b/(a b): the special-function unit (16 a
-// cycle and SM) would otherwise bound the backward, which evaluates the gate
-// twice per element.  a b overflows only where both are below about -44 (a
-// sigmoid of 1e-19), or one below -88: those pairs take two reciprocals.
+// Sigmoid of a pair, from -pre.  fp32 storage: expf and an IEEE division.  bf16
+// storage: the hardware exponential and reciprocal (a few 2^-22, far below
+// bf16's 2^-9), and one reciprocal for both, 1/a = b/(a b): the special-function
+// unit (16 a cycle and SM) would otherwise bound the backward, which evaluates
+// the gate twice per element.  The exponents are held at 2^63, so that a b
+// cannot overflow: a sigmoid below 1e-19 comes out as 1e-19.
 template <typename T>
-__device__ __forceinline__ f2 sigmoid2(f2 pre) {
+__device__ __forceinline__ float2 sigmoid2(f2 npre) {
   if constexpr (sizeof(T) == 4) {
-    const float2 v = f2_unpack(pre);
-    return f2_pack(1.f / (1.f + expf(-v.x)), 1.f / (1.f + expf(-v.y)));
+    const float2 v = f2_unpack(npre);
+    return make_float2(1.f / (1.f + expf(v.x)), 1.f / (1.f + expf(v.y)));
   } else {
-    const float2 m = f2_unpack(f2_mul(pre, f2_splat(-1.4426950408889634f)));
-    const f2 ab = f2_add(f2_pack(ex2_fast(m.x), ex2_fast(m.y)), f2_splat(1.f));
-    const float2 d = f2_unpack(ab);
-    const float p = d.x * d.y;
-    if (p < 1e37f) {
-      const float r = rcp_fast(p);
-      return f2_mul(f2_pack(d.y, d.x), f2_splat(r));
-    }
-    return f2_pack(rcp_fast(d.x), rcp_fast(d.y));
+    const float2 m = f2_unpack(f2_mul(npre, f2_splat(1.4426950408889634f)));
+    const f2 e = f2_pack(ex2_fast(fminf(m.x, 63.f)), ex2_fast(fminf(m.y, 63.f)));
+    const float2 d = f2_unpack(f2_add(e, f2_splat(1.f)));
+    const float r = rcp_fast(d.x * d.y);
+    return make_float2(d.y * r, d.x * r);
   }
 }
+// The activation works on -pre (its scale and shift are negated), which spares
+// the negations of the exponent and of the gate.
 template <typename T, int ACT>
-__device__ __forceinline__ f2 gn_act(f2 pre, float slope) {
+__device__ __forceinline__ f2 gn_act(f2 npre, float slope) {
   if constexpr (ACT == GBN_ACT_SILU) {
-    return f2_mul(pre, sigmoid2<T>(pre));
+    const float2 s = sigmoid2<T>(npre), v = f2_unpack(npre);  // a NaN stays one
+    return f2_pack(v.x * -s.x, v.y * -s.y);
   } else if constexpr (ACT == GBN_ACT_NONE) {
-    return pre;
+    return f2_neg(npre);
   } else {
-    const float2 v = f2_unpack(pre);
+    const float2 v = f2_unpack(f2_neg(npre));
     return f2_pack(v.x > 0.f ? v.x : (ACT == GBN_ACT_RELU ? 0.f : v.x * slope),
                    v.y > 0.f ? v.y : (ACT == GBN_ACT_RELU ? 0.f : v.y * slope));
   }
 }
-// d * (d act / d pre)
+// d * (d act / d pre); for SILU the derivative is s (1 + pre (1 - s)).
 template <typename T, int ACT>
-__device__ __forceinline__ f2 gn_gated(f2 d, f2 pre, float slope) {
+__device__ __forceinline__ f2 gn_gated(f2 d, f2 npre, float slope) {
   if constexpr (ACT == GBN_ACT_SILU) {
-    const f2 s = sigmoid2<T>(pre);
-    const f2 w = f2_fma(s ^ 0x8000000080000000ull, s, s);  // s (1 - s)
-    return f2_mul(d, f2_fma(pre, w, s));
+    const float2 t = sigmoid2<T>(npre);
+    const f2 s = f2_pack(t.x, t.y);
+    return f2_mul(f2_mul(d, s), f2_fma(npre, s, f2_sub(f2_splat(1.f), npre)));
   } else if constexpr (ACT == GBN_ACT_NONE) {
     return d;
   } else {
-    const float2 v = f2_unpack(pre);
+    const float2 v = f2_unpack(npre);
     const float neg = ACT == GBN_ACT_RELU ? 0.f : slope;
-    return f2_mul(d, f2_pack(v.x > 0.f ? 1.f : neg, v.y > 0.f ? 1.f : neg));
+    return f2_mul(d, f2_pack(v.x < 0.f ? 1.f : neg, v.y < 0.f ? 1.f : neg));
   }
 }
 
@@ -198,135 +181,154 @@ __device__ __forceinline__ void mom_add(Mom& a, const Mom& b) {
   a.n = n;
 }
 
-// Lanes that share a group's channels: the power of two that holds Cg, at most 32.
-__device__ __forceinline__ int group_lanes(int Cg) {
-  int l = 1;
-  while (l < 32 && l < Cg) l *= 2;
-  return l;
-}
-
 // ---------------------------------------------------------- statistics --
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kGThreads, 3) gn_stats_kernel(GnArgs a) {
-  constexpr int U = 8;  // rows of a chunk
+__global__ void __launch_bounds__(kGThreads, 3) gn_stats_kernel(const GnArgs a) {
+  constexpr int U = 4;  // rows of a chunk
+  constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   __shared__ float2 acc[kGThreads * VEC];  // [ty][channel of the tile]: mean - K, M2
-  __shared__ float cnt[kGThreads];         // [ty]
   __shared__ float Ks[kGThreads * VEC];    // shifts: x[n, 0, c]
   const GnGeom& g = a.g;
   const GnBlock b = gn_block<VEC>(g);
   pdl_launch_dependents();
   const T* xs = static_cast<const T*>(a.x) + (int64_t)b.n * g.S * g.C;
   const int W = g.TX * VEC;  // channels of a full tile
-  float cn = 0.f;
   if (b.active) {
     const T* p = xs + (int64_t)b.cv * VEC;
-    float K[VEC], mean[VEC], M2[VEC];
-    V::cvt(V::ld(p), K);
+    const T* xr = xs + (int64_t)b.r0 * g.C;
+    uint32_t q = b.off;
+    typename V::raw raw[U];
+    // rows past the last repeat the chunk's first row (a difference of 0)
+    auto load = [&](uint32_t at, int left) {
+      if (left >= U) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) mean[e] = M2[e] = 0.f;
-    const int64_t step = (int64_t)g.TY * g.C;
-    const T* q = p + (int64_t)(b.r0 + b.ty) * g.C;
-    int left = b.r1 - b.r0 > b.ty ? (b.r1 - b.r0 - b.ty + g.TY - 1) / g.TY : 0;
-    for (; left > 0; left -= U, q += U * step) {
-      typename V::raw raw[U];
+        for (int u = 0; u < U; ++u) raw[u] = V::ld(xr + (at + u * b.step));
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = V::ld(xr + (at + (u < left ? u * b.step : 0u)));
+      }
+    };
+    int left = b.left;
+    if (left > 0) load(q, left);
+    f2 K[NP], mean[NP], M2[NP];
+    to_pairs<T, VEC>(V::ld(p), K);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) mean[k] = M2[k] = 0ull;
+    float cn = 0.f;
+    while (left > 0) {
+      f2 x0[NP], s[NP], sq[NP];
+      to_pairs<T, VEC>(raw[0], x0);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) s[k] = sq[k] = 0ull;
+#pragma unroll
+      for (int u = 1; u < U; ++u) {
+        f2 v[NP];
+        to_pairs<T, VEC>(raw[u], v);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const f2 d = f2_sub(v[k], x0[k]);
+          s[k] = f2_add(s[k], d);
+          sq[k] = f2_fma(d, d, sq[k]);
+        }
+      }
       const int m = min(left, U);
+      left -= U;
+      q += U * b.step;
+      if (left > 0) load(q, left);
+      const float fm = (float)m, tot = cn + fm;
+      const float inv = m == U ? 1.f / U : __fdividef(1.f, fm), w = __fdividef(fm, tot);
+      const f2 inv2 = f2_splat(inv), w2 = f2_splat(w), ww2 = f2_splat(cn * w);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < m) raw[u] = V::ld(q + u * step);
-      float cm[VEC], cs[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) cm[e] = cs[e] = 0.f;
-      const float fm = (float)m, inv = __fdividef(1.f, fm);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < m) {
-          float v[VEC];
-          V::cvt(raw[u], v);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) cm[e] += v[e] - K[e];
-        }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) cm[e] *= inv;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < m) {
-          float v[VEC];
-          V::cvt(raw[u], v);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float d = (v[e] - K[e]) - cm[e];
-            cs[e] = fmaf(d, d, cs[e]);
-          }
-        }
-      const float tot = cn + fm, w = __fdividef(fm, tot), ww = cn * w;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = cm[e] - mean[e];
-        mean[e] = fmaf(d, w, mean[e]);
-        M2[e] = fmaf(d * d, ww, M2[e] + cs[e]);
+      for (int k = 0; k < NP; ++k) {
+        const f2 sm = f2_mul(s[k], inv2);                      // mean - x0
+        const f2 cs = f2_fma(f2_neg(sm), s[k], sq[k]);         // sum (x - mean)^2
+        const f2 d = f2_sub(f2_add(f2_sub(x0[k], K[k]), sm), mean[k]);
+        mean[k] = f2_fma(d, w2, mean[k]);
+        M2[k] = f2_fma(f2_mul(d, d), ww2, f2_add(M2[k], cs));
       }
       cn = tot;
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      acc[b.ty * W + b.tx * VEC + e] = make_float2(mean[e], M2[e]);
-      if (b.ty == 0) Ks[b.tx * VEC + e] = K[e];
+      const float2 m = f2_unpack(mean[e / 2]), v = f2_unpack(M2[e / 2]), k = f2_unpack(K[e / 2]);
+      acc[b.ty * W + b.tx * VEC + e] = (e & 1) ? make_float2(m.y, v.y) : make_float2(m.x, v.x);
+      if (b.ty == 0) Ks[b.tx * VEC + e] = (e & 1) ? k.y : k.x;
     }
-    if (b.tx == 0) cnt[b.ty] = cn;
   }
   __syncthreads();
-  // the thread rows of every channel
-  int P = 1;
-  while (P < g.TY) P *= 2;
-  for (int step = P / 2; step >= 1; step /= 2) {
-    float nn = 0.f;
-    const bool on = b.active && b.ty < step && b.ty + step < g.TY;
-    if (on) {
-      const float n1 = cnt[b.ty + step];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int i = b.ty * W + b.tx * VEC + e;
-        const float2 u = acc[i], v = acc[i + step * W];
-        Mom m{cn, u.x, u.y};
-        mom_add(m, Mom{n1, v.x, v.y});
-        acc[i] = make_float2(m.mean, m.M2);
+  // The thread rows of every channel and the channels of every group, means
+  // relative to the group's first channel in the tile, two passes each: no
+  // squares of differences from far shifts.  Thread row ty has full or full + 1
+  // rows.
+  const int full = fast_div(b.rows, g.dTY), rest = b.rows - full * g.TY;
+  auto weight = [&](int ty) { return (float)(full + (ty < rest ? 1 : 0)); };
+  const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto write = [&](int gi, float Kg, float mean, float q) {
+    // relative to the shift of the group's first channel overall
+    const float K0 = gi * g.Cg >= b.c0 ? Kg : to_f32(xs[gi * g.Cg]);
+    a.gpart[((int64_t)b.n * g.slices + b.slice) * g.E + gi + b.tile] =
+        make_float2((Kg - K0) + mean, q);
+    if (b.slice == 0 && gi * g.Cg >= b.c0) a.cpart[(int64_t)b.n * g.G + gi] = K0;
+  };
+  if (g.TY <= kGnFewRows) {
+    // a thread per channel over the thread rows, then teams of lanes over the
+    // channels of a group
+    const float inv = __fdividef(1.f, (float)b.rows);
+    for (int c = threadIdx.x; c < b.c1 - b.c0; c += blockDim.x) {
+      float s = 0.f, q = 0.f;
+      for (int ty = 0; ty < g.TY; ++ty) s = fmaf(weight(ty), acc[ty * W + c].x, s);
+      const float mean = s * inv;
+      for (int ty = 0; ty < g.TY; ++ty) {
+        const float2 v = acc[ty * W + c];
+        const float d = v.x - mean;
+        q += fmaf(weight(ty) * d, d, v.y);
       }
-      cn += n1;
-      nn = cn;
+      acc[c] = make_float2(mean, q);  // row 0 of the channel: only this thread reads it
     }
     __syncthreads();
-    if (on && b.tx == 0) cnt[b.ty] = nn;
-    __syncthreads();
-  }
-  // The channels of every group of the tile, relative to the group's first
-  // channel in the tile: teams of lanes, two passes (equal counts).
-  const int L = group_lanes(g.Cg), lane = threadIdx.x & (L - 1);
-  const int teams = blockDim.x / L;
-  const float rows = (float)(b.r1 - b.r0);
-  for (int gb = b.g0; gb < b.g1; gb += teams) {
-    const int gi = gb + threadIdx.x / L;
-    const bool on = gi < b.g1;
-    const int ca = on ? max(gi * g.Cg, b.c0) - b.c0 : 0;
-    const int cb = on ? min((gi + 1) * g.Cg, b.c1) - b.c0 : 0;
-    const float Kg = on ? Ks[ca] : 0.f;
-    float s = 0.f;
-    for (int c = ca + lane; c < cb; c += L) s += (Ks[c] - Kg) + acc[c].x;
-    for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float nc = (float)(cb - ca), mean = s / nc;
-    float q = 0.f;
-    for (int c = ca + lane; c < cb; c += L) {
-      const float d = ((Ks[c] - Kg) + acc[c].x) - mean;
-      q += fmaf(rows * d, d, acc[c].y);
+    const int L = 1 << g.llc, l = lane & (L - 1), teams = blockDim.x >> g.llc;
+    for (int gb = b.g0; gb < b.g1; gb += teams) {
+      const int gi = gb + (threadIdx.x >> g.llc);
+      const bool on = gi < b.g1;
+      const int ca = on ? max(gi * g.Cg, b.c0) - b.c0 : 0;
+      const int cb = on ? min((gi + 1) * g.Cg, b.c1) - b.c0 : 0;
+      const float Kg = Ks[ca];
+      float s = 0.f, q = 0.f;
+      for (int c = ca + l; c < cb; c += L) s += (Ks[c] - Kg) + acc[c].x;
+      for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float mean = __fdividef(s, (float)(cb - ca));
+      for (int c = ca + l; c < cb; c += L) {
+        const float2 v = acc[c];
+        const float d = ((Ks[c] - Kg) + v.x) - mean;
+        q += fmaf((float)b.rows * d, d, v.y);
+      }
+      for (int o = L / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+      if (on && l == 0) write(gi, Kg, mean, q);
     }
-    for (int o = L / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-    if (on && lane == 0) {
-      // relative to the shift of the group's first channel overall
-      const float K0 = gi * g.Cg >= b.c0 ? Kg : to_f32(xs[gi * g.Cg]);
-      a.gpart[((int64_t)b.n * g.slices + b.slice) * g.E + gi + b.tile] =
-          make_float2((Kg - K0) + mean, q);
-      if (b.slice == 0 && gi * g.Cg >= b.c0) a.cpart[(int64_t)b.n * g.G + gi] = K0;
+  } else {
+    // few channels, many thread rows: a warp per group, lanes over both
+    const int Lc = 1 << g.llc, lc = lane & (Lc - 1), lt = lane >> g.llc, Lt = 32 >> g.llc;
+    for (int gi = b.g0 + warp; gi < b.g1; gi += nw) {
+      const int ca = max(gi * g.Cg, b.c0) - b.c0, cb = min((gi + 1) * g.Cg, b.c1) - b.c0;
+      const float Kg = Ks[ca];
+      float s = 0.f, q = 0.f;
+      for (int c = ca + lc; c < cb; c += Lc) {
+        const float dk = Ks[c] - Kg;
+        for (int ty = lt; ty < g.TY; ty += Lt) s = fmaf(weight(ty), dk + acc[ty * W + c].x, s);
+      }
+      const float mean = __fdividef(warp_sum(s), (float)b.rows * (float)(cb - ca));
+      for (int c = ca + lc; c < cb; c += Lc) {
+        const float dk = (Ks[c] - Kg) - mean;
+        for (int ty = lt; ty < g.TY; ty += Lt) {
+          const float2 v = acc[ty * W + c];
+          const float d = dk + v.x;
+          q += fmaf(weight(ty) * d, d, v.y);
+        }
+      }
+      q = warp_sum(q);
+      if (lane == 0) write(gi, Kg, mean, q);
     }
   }
   pdl_wait();  // the previous launch of this call (another run of samples) is complete too
@@ -340,9 +342,8 @@ __device__ __forceinline__ void gn_tiles_of(const GnGeom& g, int gi, int& t0, in
     t1 = 1;
     return;
   }
-  const int W = g.TX * VEC;
-  t0 = gi * g.Cg / W;
-  t1 = ((gi + 1) * g.Cg - 1) / W + 1;
+  t0 = (int)fast_div(gi * g.Cg / VEC, g.dTX);
+  t1 = (int)fast_div(((gi + 1) * g.Cg - 1) / VEC, g.dTX) + 1;
 }
 
 // Walks the partials of the tile's groups: thread row q of R takes slices q,
@@ -354,9 +355,8 @@ template <int VEC, typename Init, typename Take, typename Done>
 __device__ __forceinline__ void gn_walk(const GnArgs& a, const GnBlock& b, Init init, Take take,
                                         Done done) {
   const GnGeom& g = a.g;
-  const int ng = b.g1 - b.g0, cols = min(ng, (int)blockDim.x);
-  const int R = blockDim.x / cols;
-  const int q = (int)threadIdx.x / cols, col = threadIdx.x - q * cols;
+  const int cols = g.cols, R = g.R;
+  const int q = (int)fast_div(threadIdx.x, g.dcols), col = threadIdx.x - q * cols;
   for (int gb = b.g0; gb < b.g1; gb += cols) {
     const int gi = gb + col;
     const bool on = q < R && gi < b.g1;
@@ -390,17 +390,48 @@ __device__ __forceinline__ void gn_walk(const GnArgs& a, const GnBlock& b, Init 
 
 // ---------------------------------------------------------------- apply --
 
+// This thread's VEC channels of a per-channel array in shared memory.
+template <int VEC>
+__device__ __forceinline__ void gn_const(const float* arr, int tx, f2 (&p)[kPairs<VEC>]) {
+  float v[VEC];
+  Vec<float, (VEC > 4 ? 4 : VEC)>::cvt(
+      Vec<float, (VEC > 4 ? 4 : VEC)>::ld(arr + tx * VEC),
+      *reinterpret_cast<float(*)[VEC > 4 ? 4 : VEC]>(&v[0]));
+  if constexpr (VEC > 4)
+    Vec<float, 4>::cvt(Vec<float, 4>::ld(arr + tx * VEC + 4), *reinterpret_cast<float(*)[4]>(&v[4]));
+#pragma unroll
+  for (int k = 0; k < kPairs<VEC>; ++k) p[k] = pair_at(v, k);
+}
+
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, 3) gn_apply_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_apply_kernel(const GnArgs a) {
   constexpr int U = 4;
-  constexpr int NP = GnP<VEC>::NP;
+  constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   extern __shared__ float3 fin[];  // per group of the tile: mean hi, lo, rstd
   __shared__ Mom red[kGThreads];
+  __shared__ __align__(16) float cst[3][kGThreads * VEC];  // per channel: mean hi, scale, shift
   const GnGeom& g = a.g;
   const GnBlock b = gn_block<VEC>(g);
-  const T* xs = static_cast<const T*>(a.x) + (int64_t)b.n * g.S * g.C;
-  T* ys = static_cast<T*>(a.out) + (int64_t)b.n * g.S * g.C;
+  const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
+  const T* xs = static_cast<const T*>(a.x) + base;
+  T* ys = static_cast<T*>(a.out) + base;
+  // The first rows are on their way while the statistics are finished.  From
+  // the slice's end: what the statistics pass read last is likeliest in L2.
+  int left = b.active ? b.left : 0;
+  uint32_t o = b.off + (uint32_t)(left - 1) * b.step;  // not used where there is no row
+  typename V::raw raw[U];
+  auto load = [&] {
+    if (left >= U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = V::ld(xs + (o - u * b.step));
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < left) raw[u] = V::ld(xs + (o - u * b.step));
+    }
+  };
+  load();
   pdl_wait();
   pdl_launch_dependents();
   Mom m{0.f, 0.f, 0.f};
@@ -434,45 +465,38 @@ __global__ void __launch_bounds__(kGThreads, 3) gn_apply_kernel(GnArgs a) {
         }
         __syncthreads();
       });
-  if (!b.active) return;
+  for (int k = threadIdx.x; k < b.c1 - b.c0; k += blockDim.x) {
+    const int c = b.c0 + k;
+    const float3 f = fin[fast_div(c, g.dCg) - b.g0];
+    const float sc = f.z * (a.gamma ? a.gamma[c] : 1.f);
+    cst[0][k] = f.x;
+    cst[1][k] = -sc;
+    cst[2][k] = -fmaf(-f.y, sc, a.beta ? a.beta[c] : 0.f);
+  }
+  __syncthreads();
+  if (left <= 0) return;
   f2 nm[NP], sc[NP], be[NP];
-  {
-    float m0[VEC], m1[VEC], m2[VEC];
+  gn_const<VEC>(cst[0], b.tx, nm);
+  gn_const<VEC>(cst[1], b.tx, sc);
+  gn_const<VEC>(cst[2], b.tx, be);
+  auto row = [&](int u) {
+    f2 v[NP];
+    to_pairs<T, VEC>(raw[u], v);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = b.cv * VEC + e;
-      const float3 f = fin[c / g.Cg - b.g0];
-      m0[e] = f.x;
-      m1[e] = f.z * (a.gamma ? a.gamma[c] : 1.f);
-      m2[e] = fmaf(-f.y, m1[e], a.beta ? a.beta[c] : 0.f);
-    }
+    for (int k = 0; k < NP; ++k)
+      v[k] = gn_act<T, ACT>(f2_fma(f2_sub(v[k], nm[k]), sc[k], be[k]), a.slope);
+    store_pairs<T, VEC>(ys + (o - u * b.step), v);
+  };
+  while (left >= U) {
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      nm[k] = gn_pair(m0, k);
-      sc[k] = gn_pair(m1, k);
-      be[k] = gn_pair(m2, k);
-    }
+    for (int u = 0; u < U; ++u) row(u);
+    left -= U;
+    o -= U * b.step;
+    load();
   }
-  // from the slice's end: what the statistics pass read last is likeliest in L2
-  const int64_t step = (int64_t)g.TY * g.C;
-  int left = b.r1 - b.r0 > b.ty ? (b.r1 - b.r0 - b.ty + g.TY - 1) / g.TY : 0;
-  int64_t o = (int64_t)(b.r0 + b.ty) * g.C + (int64_t)(left - 1) * step + (int64_t)b.cv * VEC;
-  for (; left > 0; left -= U, o -= U * step) {
-    typename V::raw raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left) raw[u] = V::ld(xs + o - u * step);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left) {
-        f2 v[NP];
-        gn_pairs<T, VEC>(raw[u], v);
-#pragma unroll
-        for (int k = 0; k < NP; ++k)
-          v[k] = gn_act<T, ACT>(f2_fma(f2_sub(v[k], nm[k]), sc[k], be[k]), a.slope);
-        gn_store<T, VEC>(ys + o - u * step, v);
-      }
-  }
+  for (int u = 0; u < U - 1; ++u)
+    if (u < left) row(u);
 }
 
 // -------------------------------------------------------- backward sums --
@@ -490,66 +514,82 @@ template <typename T> struct GnSum {
 // Per channel of the tile: sum e and sum e*xhat of the block's rows, to the
 // column partials; and per group the sums of gamma*e and gamma*e*xhat.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, 2) gn_sums_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_sums_kernel(const GnArgs a) {
   constexpr int U = 4;  // rows in flight (two inputs)
-  constexpr int NP = GnP<VEC>::NP;
+  constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
-  __shared__ DF sa[kGThreads * VEC], sb[kGThreads * VEC];  // [ty][channel]
+  __shared__ __align__(16) DF sab[2][kGThreads * VEC];  // [ty][channel]
+  DF* sa = sab[0];
+  DF* sb = sab[1];
   const GnGeom& g = a.g;
   const GnBlock b = gn_block<VEC>(g);
   pdl_launch_dependents();
-  const int64_t off = (int64_t)b.n * g.S * g.C;
-  const T* xs = static_cast<const T*>(a.x) + off;
-  const T* ds = static_cast<const T*>(a.dy) + off;
+  const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
+  const T* xs = static_cast<const T*>(a.x) + base;
+  const T* ds = static_cast<const T*>(a.dy) + base;
   const int W = g.TX * VEC;
   const int64_t ng = (int64_t)g.N * g.G, so = (int64_t)b.n * g.G;
+  float* cst = reinterpret_cast<float*>(sa);  // per channel: mean hi, scale, shift
+  for (int k = threadIdx.x; k < b.c1 - b.c0; k += blockDim.x) {
+    const int c = b.c0 + k, gi = fast_div(c, g.dCg);
+    const float s1 = a.stats[ng + so + gi] * (a.gamma ? a.gamma[c] : 1.f);
+    cst[k] = a.stats[so + gi];
+    cst[kGThreads * VEC + k] = -s1;
+    cst[2 * kGThreads * VEC + k] = -fmaf(-a.stats[2 * ng + so + gi], s1, a.beta ? a.beta[c] : 0.f);
+  }
+  __syncthreads();
+  f2 nm[NP], sc[NP], be[NP];
+  gn_const<VEC>(cst, b.tx, nm);
+  gn_const<VEC>(cst + kGThreads * VEC, b.tx, sc);
+  gn_const<VEC>(cst + 2 * kGThreads * VEC, b.tx, be);
+  __syncthreads();  // the sums below reuse the memory
   if (b.active) {
-    f2 nm[NP], sc[NP], be[NP];
     GnSum<T> A[NP], B[NP];
-    {
-      float m0[VEC], m1[VEC], m2[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int c = b.cv * VEC + e, gi = c / g.Cg;
-        m0[e] = a.stats[so + gi];
-        m1[e] = a.stats[ng + so + gi] * (a.gamma ? a.gamma[c] : 1.f);
-        m2[e] = fmaf(-a.stats[2 * ng + so + gi], m1[e], a.beta ? a.beta[c] : 0.f);
-      }
+    uint32_t o = b.off;
+    int left = b.left;
+    f2 ca[NP], cb[NP];
+    auto row = [&](typename V::raw rx, typename V::raw rd) {
+      f2 v[NP], d[NP];
+      to_pairs<T, VEC>(rx, v);
+      to_pairs<T, VEC>(rd, d);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        nm[k] = gn_pair(m0, k);
-        sc[k] = gn_pair(m1, k);
-        be[k] = gn_pair(m2, k);
+        const f2 xc = f2_sub(v[k], nm[k]);
+        const f2 t = gn_gated<T, ACT>(d[k], f2_fma(xc, sc[k], be[k]), a.slope);
+        ca[k] = f2_add(ca[k], t);
+        cb[k] = f2_fma(t, xc, cb[k]);
       }
-    }
-    const int64_t step = (int64_t)g.TY * g.C;
-    int64_t o = (int64_t)(b.r0 + b.ty) * g.C + (int64_t)b.cv * VEC;
-    int left = b.r1 - b.r0 > b.ty ? (b.r1 - b.r0 - b.ty + g.TY - 1) / g.TY : 0;
-    for (; left > 0; left -= U, o += U * step) {
+    };
+    for (; left >= U; left -= U, o += U * b.step) {
       typename V::raw rx[U], rd[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < left) {
-          rx[u] = V::ld(xs + o + u * step);
-          rd[u] = V::ld(ds + o + u * step);
-        }
-      f2 ca[NP], cb[NP];
+      for (int u = 0; u < U; ++u) {
+        rx[u] = V::ld(xs + (o + u * b.step));
+        rd[u] = V::ld(ds + (o + u * b.step));
+      }
 #pragma unroll
       for (int k = 0; k < NP; ++k) ca[k] = cb[k] = 0ull;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < left) {
-          f2 v[NP], d[NP];
-          gn_pairs<T, VEC>(rx[u], v);
-          gn_pairs<T, VEC>(rd[u], d);
+      for (int u = 0; u < U; ++u) row(rx[u], rd[u]);
 #pragma unroll
-          for (int k = 0; k < NP; ++k) {
-            const f2 xc = f2_sub(v[k], nm[k]);
-            const f2 t = gn_gated<T, ACT>(d[k], f2_fma(xc, sc[k], be[k]), a.slope);
-            ca[k] = f2_add(ca[k], t);
-            cb[k] = f2_fma(t, xc, cb[k]);
-          }
+      for (int k = 0; k < NP; ++k) {
+        A[k].add(ca[k]);
+        B[k].add(cb[k]);
+      }
+    }
+    if (left > 0) {
+      typename V::raw rx[U - 1], rd[U - 1];
+#pragma unroll
+      for (int u = 0; u < U - 1; ++u)
+        if (u < left) {
+          rx[u] = V::ld(xs + (o + u * b.step));
+          rd[u] = V::ld(ds + (o + u * b.step));
         }
+#pragma unroll
+      for (int k = 0; k < NP; ++k) ca[k] = cb[k] = 0ull;
+#pragma unroll
+      for (int u = 0; u < U - 1; ++u)
+        if (u < left) row(rx[u], rd[u]);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         A[k].add(ca[k]);
@@ -582,23 +622,21 @@ __global__ void __launch_bounds__(kGThreads, 2) gn_sums_kernel(GnArgs a) {
   // sum e*xhat = rstd*(sum e*(x - mean_hi) - mean_lo*sum e)
   const int64_t row = (int64_t)b.n * g.slices + b.slice, rows = (int64_t)g.N * g.slices;
   for (int k = threadIdx.x; k < b.c1 - b.c0; k += blockDim.x) {
-    const int c = b.c0 + k, gi = c / g.Cg;
+    const int c = b.c0 + k, gi = fast_div(c, g.dCg);
     const DF A = sa[k];
     const DF dg = df_norm(df_mul(df_sum(sb[k], df_neg(df_mul(A, a.stats[2 * ng + so + gi]))),
                                  a.stats[ng + so + gi]));
     float* p = a.cpart + row * g.C + c;
-    p[0] = dg.hi;
-    p[rows * g.C] = dg.lo;
-    p[2 * rows * g.C] = A.hi;
-    p[3 * rows * g.C] = A.lo;
+    p[0] = df_round(dg);
+    p[rows * g.C] = df_round(A);
     const float gm = a.gamma ? a.gamma[c] : 1.f;
     sa[k] = DF{gm * df_round(A), gm * df_round(dg)};
   }
   __syncthreads();
-  const int L = group_lanes(g.Cg), lane = threadIdx.x & (L - 1);
-  const int teams = blockDim.x / L;
+  const int L = 1 << g.llc, lane = threadIdx.x & (L - 1);
+  const int teams = blockDim.x >> g.llc;
   for (int gb = b.g0; gb < b.g1; gb += teams) {
-    const int gi = gb + threadIdx.x / L;
+    const int gi = gb + (threadIdx.x >> g.llc);
     const bool on = gi < b.g1;
     const int ca = on ? max(gi * g.Cg, b.c0) - b.c0 : 0;
     const int cb = on ? min((gi + 1) * g.Cg, b.c1) - b.c0 : 0;
@@ -616,22 +654,106 @@ __global__ void __launch_bounds__(kGThreads, 2) gn_sums_kernel(GnArgs a) {
   pdl_wait();  // the previous launch of this call (another run of samples) is complete too
 }
 
+// ------------------------------------------------------- weight gradients --
+
+// dgamma and dbeta: the channel partials of every sample and slice, added in a
+// fixed order.  A cluster of eight blocks per 32 channels: each block takes an
+// eighth of the rows (32 thread rows, eight rows in flight), and the eight sums
+// meet in the first block's shared memory.
+constexpr int kGnWCluster = 8;
+__global__ void __cluster_dims__(kGnWCluster, 1, 1) __launch_bounds__(1024)
+    gn_weight_kernel(const float* __restrict__ part, int64_t rows, int C, float* dgamma,
+                     float* dbeta) {
+  __shared__ DF sm[2][32][33];
+  __shared__ DF all[kGnWCluster][2][32];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int rank = blockIdx.x % kGnWCluster, c = (blockIdx.x / kGnWCluster) * 32 + tx;
+  const int64_t r0 = rows * rank / kGnWCluster, r1 = rows * (rank + 1) / kGnWCluster;
+  pdl_wait();
+  DF s[2] = {{0.f, 0.f}, {0.f, 0.f}};
+  if (c < C) {
+    constexpr int U = 4;
+    for (int64_t r = r0 + ty; r < r1; r += 32 * U) {
+      float v[2][U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool ok = r + 32 * u < r1;
+        v[0][u] = ok ? __ldcg(part + (r + 32 * u) * C + c) : 0.f;
+        v[1][u] = ok ? __ldcg(part + (rows + r + 32 * u) * C + c) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        df_add(s[0], v[0][u]);
+        df_add(s[1], v[1][u]);
+      }
+    }
+  }
+  sm[0][ty][tx] = s[0];
+  sm[1][ty][tx] = s[1];
+  __syncthreads();
+  // two warps a sum: lanes over the thread rows of a channel
+  for (int k = ty; k < 64; k += 32) {
+    const DF t = warp_sum_df(sm[k >> 5][tx][k & 31]);
+    if (tx == 0) {
+      // into block 0's shared memory
+      const uint32_t at = smem_u32(&all[rank][k >> 5][k & 31]);
+      asm volatile(
+          "{\n\t.reg .b32 a;\n\t"
+          "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+          "st.shared::cluster.v2.f32 [a], {%1, %2};\n\t}" ::"r"(at),
+          "f"(t.hi), "f"(t.lo)
+          : "memory");
+    }
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+  if (rank == 0 && ty < 2 && c < C) {
+    DF t = all[0][ty][tx];
+#pragma unroll
+    for (int q = 1; q < kGnWCluster; ++q) t = df_sum(t, all[q][ty][tx]);
+    float* out = ty == 0 ? dgamma : dbeta;
+    if (out != nullptr) out[c] = df_round(t);
+  }
+}
+
 // ------------------------------------------------------------------- dx --
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, 2) gn_dx_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_dx_kernel(const GnArgs a) {
   constexpr int U = 4;
-  constexpr int NP = GnP<VEC>::NP;
+  constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   extern __shared__ float2 kk[];  // per group of the tile: k0, k1
   __shared__ float2 red[kGThreads];
+  __shared__ __align__(16) float cst[6][kGThreads * VEC];  // per channel
   const GnGeom& g = a.g;
   const GnBlock b = gn_block<VEC>(g);
-  const int64_t off = (int64_t)b.n * g.S * g.C;
-  const T* xs = static_cast<const T*>(a.x) + off;
-  const T* ds = static_cast<const T*>(a.dy) + off;
-  T* os = static_cast<T*>(a.out) + off;
+  const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
+  const T* xs = static_cast<const T*>(a.x) + base;
+  const T* ds = static_cast<const T*>(a.dy) + base;
+  T* os = static_cast<T*>(a.out) + base;
   const int64_t ng = (int64_t)g.N * g.G, so = (int64_t)b.n * g.G;
+  // the first rows are on their way while the group sums are finished
+  int left = b.active ? b.left : 0;
+  uint32_t o = b.off + (uint32_t)(left - 1) * b.step;  // not used where there is no row
+  typename V::raw rx[U], rd[U];
+  auto load = [&] {
+    if (left >= U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rx[u] = V::ld(xs + (o - u * b.step));
+        rd[u] = V::ld(ds + (o - u * b.step));
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < left) {
+          rx[u] = V::ld(xs + (o - u * b.step));
+          rd[u] = V::ld(ds + (o - u * b.step));
+        }
+    }
+  };
+  load();
   pdl_wait();
   pdl_launch_dependents();
   float2 m = make_float2(0.f, 0.f);
@@ -659,57 +781,50 @@ __global__ void __launch_bounds__(kGThreads, 2) gn_dx_kernel(GnArgs a) {
         }
         __syncthreads();
       });
-  if (!b.active) return;
   // dx = sc*e + (x - mean_hi)*q1 + q0
-  f2 nm[NP], sc[NP], be[NP], q1[NP], q0[NP];
-  {
-    float m0[VEC], m1[VEC], m2[VEC], m3[VEC], m4[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = b.cv * VEC + e, gi = c / g.Cg;
-      const float rstd = a.stats[ng + so + gi], ml = a.stats[2 * ng + so + gi];
-      const float2 k = kk[gi - b.g0];
-      m0[e] = a.stats[so + gi];
-      m1[e] = rstd * (a.gamma ? a.gamma[c] : 1.f);
-      m2[e] = fmaf(-ml, m1[e], a.beta ? a.beta[c] : 0.f);
-      m3[e] = -(rstd * rstd) * k.y;
-      m4[e] = -fmaf(ml, m3[e], rstd * k.x);
-    }
+  for (int k = threadIdx.x; k < b.c1 - b.c0; k += blockDim.x) {
+    const int c = b.c0 + k, gi = fast_div(c, g.dCg);
+    const float rstd = a.stats[ng + so + gi], ml = a.stats[2 * ng + so + gi];
+    const float2 kg = kk[gi - b.g0];
+    const float s1 = rstd * (a.gamma ? a.gamma[c] : 1.f), q1 = -(rstd * rstd) * kg.y;
+    cst[0][k] = a.stats[so + gi];
+    cst[1][k] = -s1;
+    cst[2][k] = -fmaf(-ml, s1, a.beta ? a.beta[c] : 0.f);
+    cst[3][k] = q1;
+    cst[4][k] = -fmaf(ml, q1, rstd * kg.x);
+    cst[5][k] = s1;
+  }
+  __syncthreads();
+  if (left <= 0) return;
+  f2 nm[NP], ns[NP], be[NP], q1[NP], q0[NP], sc[NP];
+  gn_const<VEC>(cst[0], b.tx, nm);
+  gn_const<VEC>(cst[1], b.tx, ns);
+  gn_const<VEC>(cst[5], b.tx, sc);
+  gn_const<VEC>(cst[2], b.tx, be);
+  gn_const<VEC>(cst[3], b.tx, q1);
+  gn_const<VEC>(cst[4], b.tx, q0);
+  auto row = [&](int u) {
+    f2 v[NP], d[NP];
+    to_pairs<T, VEC>(rx[u], v);
+    to_pairs<T, VEC>(rd[u], d);
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      nm[k] = gn_pair(m0, k);
-      sc[k] = gn_pair(m1, k);
-      be[k] = gn_pair(m2, k);
-      q1[k] = gn_pair(m3, k);
-      q0[k] = gn_pair(m4, k);
+      const f2 xc = f2_sub(v[k], nm[k]);
+      const f2 t = gn_gated<T, ACT>(d[k], f2_fma(xc, ns[k], be[k]), a.slope);
+      v[k] = f2_fma(t, sc[k], f2_fma(xc, q1[k], q0[k]));
     }
+    store_pairs<T, VEC>(os + (o - u * b.step), v);
+  };
+  while (left >= U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) row(u);
+    left -= U;
+    o -= U * b.step;
+    load();
   }
-  const int64_t step = (int64_t)g.TY * g.C;
-  int left = b.r1 - b.r0 > b.ty ? (b.r1 - b.r0 - b.ty + g.TY - 1) / g.TY : 0;
-  int64_t o = (int64_t)(b.r0 + b.ty) * g.C + (int64_t)(left - 1) * step + (int64_t)b.cv * VEC;
-  for (; left > 0; left -= U, o -= U * step) {
-    typename V::raw rx[U], rd[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left) {
-        rx[u] = V::ld(xs + o - u * step);
-        rd[u] = V::ld(ds + o - u * step);
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left) {
-        f2 v[NP], d[NP];
-        gn_pairs<T, VEC>(rx[u], v);
-        gn_pairs<T, VEC>(rd[u], d);
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const f2 xc = f2_sub(v[k], nm[k]);
-          const f2 t = gn_gated<T, ACT>(d[k], f2_fma(xc, sc[k], be[k]), a.slope);
-          v[k] = f2_fma(t, sc[k], f2_fma(xc, q1[k], q0[k]));
-        }
-        gn_store<T, VEC>(os + o - u * step, v);
-      }
-  }
+  for (int u = 0; u < U - 1; ++u)
+    if (u < left) row(u);
 }
 
 // ----------------------------------------------------------------- host --
@@ -720,16 +835,18 @@ template <typename T, int VEC, int ACT>
 cudaError_t gn_run(GnKernel k, const GnPlan& p, const GnArgs& a, cudaStream_t st) {
   const bool chained = a.g.n0 > 0;  // not the call's first launch
   const int64_t n = p.N - a.g.n0 < p.run ? p.N - a.g.n0 : p.run;
-  const dim3 grid((unsigned)(n * p.slices * p.tiles)), block((unsigned)p.threads);
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.slices, (unsigned)n);
+  const dim3 block((unsigned)p.threads);
   const size_t smem = (size_t)p.tile_groups;
-  switch (k) {
-    case kGnStats: return launch(gn_stats_kernel<T, VEC>, grid, block, 0, st, chained, a);
-    case kGnApply:
-      return launch(gn_apply_kernel<T, VEC, ACT>, grid, block, smem * sizeof(float3), st, true, a);
-    case kGnSums: return launch(gn_sums_kernel<T, VEC, ACT>, grid, block, 0, st, chained, a);
-    default:
-      return launch(gn_dx_kernel<T, VEC, ACT>, grid, block, smem * sizeof(float2), st, true, a);
+  if (k == kGnStats) return launch(gn_stats_kernel<T, VEC>, grid, block, 0, st, chained, a);
+  if (k == kGnApply)
+    return launch(gn_apply_kernel<T, VEC, ACT>, grid, block, smem * sizeof(float3), st, true, a);
+  if constexpr (VEC <= 4) {  // the backward's widest (gn_plan)
+    if (k == kGnSums)
+      return launch(gn_sums_kernel<T, VEC, ACT>, grid, block, 0, st, chained, a);
+    return launch(gn_dx_kernel<T, VEC, ACT>, grid, block, smem * sizeof(float2), st, true, a);
   }
+  return cudaErrorInvalidValue;
 }
 template <typename T, int VEC>
 cudaError_t gn_run_act(GnKernel k, int act, const GnPlan& p, const GnArgs& a, cudaStream_t st) {
@@ -771,6 +888,13 @@ GnArgs gn_args(const GnPlan& p, void* ws) {
   a.g.slices = p.slices;
   a.g.rps = p.rps;
   a.g.E = (int32_t)(p.G + p.tiles - 1);
+  a.g.cols = p.tile_groups < p.threads ? p.tile_groups : p.threads;
+  a.g.R = p.threads / a.g.cols;
+  while (a.g.llc < 5 && (1 << a.g.llc) < a.g.Cg) ++a.g.llc;
+  a.g.dTX = make_fast_div((uint32_t)p.TX);
+  a.g.dTY = make_fast_div((uint32_t)p.TY);
+  a.g.dCg = make_fast_div((uint32_t)a.g.Cg);
+  a.g.dcols = make_fast_div((uint32_t)a.g.cols);
   a.gpart = static_cast<float2*>(ws);
   a.cpart = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + p.gpart_bytes);
   return a;
@@ -794,29 +918,35 @@ bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, int64_t esize,
   if (p->TY > S) p->TY = (int)S;
   p->threads = (p->TX * p->TY + 31) / 32 * 32;
   const int64_t W = (int64_t)p->TX * vec, Cg = C / G;
-  p->tile_groups = (int)((W + Cg - 1) / Cg + 1);
+  p->tile_groups = (int)((W + Cg - 1) / Cg + 1);  // cut at both ends
+  if (p->tile_groups > G) p->tile_groups = (int)G;
   // Samples per pair of launches: runs whose inputs stay in half of L2 between
   // the two passes, so the second one reads no DRAM.
   const int64_t sample = S * C * esize * (backward ? 2 : 1);
   int64_t run = (int64_t)dev.l2_bytes / 2 / (sample > 0 ? sample : 1);
   if (run < 1) run = 1;
   if (run > N) run = N;
+  if (run > 65535) run = 65535;  // grid z
   run = (N + (N + run - 1) / run - 1) / ((N + run - 1) / run);  // even runs
   p->run = run;
   // the resident block slots once over a run's samples, at least one round of
   // loads a thread
-  const int64_t slots = (int64_t)dev.sms * (backward ? 2 : 3);
-  const int64_t per = (slots + run * p->tiles - 1) / (run * p->tiles);
-  const int64_t round = (int64_t)p->TY * (backward ? 4 : 8);
+  const int64_t slots = (int64_t)dev.sms * (backward && esize * vec <= 8 ? 4 : 3);
+  const int64_t per = slots / (run * p->tiles);
+  const int64_t round = (int64_t)p->TY * 4;
   const int64_t rounds = (S + round - 1) / round;
   int64_t s = per < rounds ? per : rounds;
   if (s < 1) s = 1;
+  // 32-bit offsets inside a slice
+  const int64_t least = (S * C * esize + ((int64_t)1 << 31) - 1) >> 31;
+  if (s < least) s = least;
   p->rps = (int)((S + s - 1) / s);
+  while ((int64_t)p->rps * C * esize > ((int64_t)1 << 31) && p->rps > 1) --p->rps;
   s = (S + p->rps - 1) / p->rps;
   p->slices = (int)s;
-  if (run * s * p->tiles > INT32_MAX) return false;
+  if (s > 65535) return false;
   p->gpart_bytes = ((size_t)N * s * (G + p->tiles - 1) * sizeof(float2) + 255) & ~(size_t)255;
-  const size_t rest = backward ? (size_t)4 * N * s * C : (size_t)N * G;
+  const size_t rest = backward ? (size_t)2 * N * s * C : (size_t)N * G;
   p->ws_bytes = p->gpart_bytes + ((rest * sizeof(float) + 255) & ~(size_t)255);
   return true;
 }
@@ -872,8 +1002,9 @@ cudaError_t gn_backward(const GnPlan& p, int dtype, const void* x, const void* d
     if (e == cudaSuccess) e = gn_dispatch(kGnDx, dtype, act, p, a, st);
   }
   if (e != cudaSuccess || (dgamma == nullptr && dbeta == nullptr)) return e;
-  void* outs[3] = {dgamma, dbeta, nullptr};
-  return colsum_launch(a.cpart, 2, 2, (int)(p.N * p.slices), p.C, GBN_F32, outs, st, true);
+  const float* part = a.cpart;
+  return launch(gn_weight_kernel, dim3((unsigned)((p.C + 31) / 32 * kGnWCluster)), dim3(1024), 0, st,
+                true, part, p.N * p.slices, (int)p.C, dgamma, dbeta);
 }
 
 }  // namespace gbn

@@ -84,8 +84,7 @@ struct LnArgs {
 // Where the fused kernels' keep decisions come from: mask bytes (or none:
 // everything kept), or the generator.
 constexpr int kMaskBytes = 0;
-constexpr int kMaskRng = 1;       // round keys from the launch's arguments
-constexpr int kMaskRngState = 2;  // seed and offset from device memory
+constexpr int kMaskRng = 1;
 
 // One element's LayerNorm input z from the stage (fused: residual +
 // keep*(input + bias), exact (hi, lo) for fp32 outputs).
@@ -153,11 +152,10 @@ __device__ __forceinline__ void keep_pairs(uint2 m, float s, f2 (&keep2)[NP]) {
 
 // All-ones words where the generator keeps the element, else zero, for the NP
 // pairs of the 16-byte vector at element i.
-template <int NP, bool STATE>
-__device__ __forceinline__ void rng_pairs(const Philox<STATE>& g, const RngArgs& a, uint64_t i,
-                                          f2 (&keep2)[NP]) {
+template <int NP>
+__device__ __forceinline__ void rng_pairs(const Philox<true>& g, uint64_t i, f2 (&keep2)[NP]) {
   bool f[2 * NP];
-  g.template keep<2 * NP>(a, i, f);
+  g.template keep<2 * NP>(i, f);
 #pragma unroll
   for (int p = 0; p < NP; ++p)
     keep2[p] = f2_pack(__uint_as_float(f[2 * p] ? 0xffffffffu : 0u),
@@ -192,7 +190,7 @@ constexpr int kLnRingWarps[3] = {0, kLnRingWarpsKV1, kLnRingWarpsKVn};
 // register budget of a thread follows from it).
 template <typename T, int KV, bool FUSED, int MASK, int MAXW>
 __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const LnArgs a) {
-  constexpr bool RNG = MASK != kMaskBytes;
+  constexpr bool RNG = MASK == kMaskRng;
   constexpr int VE = 16 / sizeof(T);
   constexpr bool COMP = sizeof(T) == 4;
   using PK = Pairs16<T>;
@@ -202,7 +200,9 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
   extern __shared__ __align__(128) unsigned char data[];
   __shared__ RowShared sh;
   __shared__ __align__(16) float red[kLnMaxRedFloats];
-  static_assert(sizeof(RowShared) + sizeof(red) + 16 <= kRowStaticSmem, "static shared memory");
+  __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  static_assert(sizeof(RowShared) + sizeof(red) + sizeof(keys) + 32 <= kRowStaticSmem,
+                "static shared memory");
 
   const int tid = threadIdx.x;
   const int g = blockIdx.x, G = gridDim.x;
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
   const bool with_res = FUSED && !a.zin;
 
   const int P = (TPRW + 3) & ~3;  // padded warp run of a slot
+  if constexpr (RNG) philox_fill(keys, a.rng);
   for (int k = tid; k < kLnMaxRedFloats; k += blockDim.x) red[k] = 0.f;  // padding stays 0
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -249,8 +250,8 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
     const int ct = tid - 32, lane = ct & 31, cw = ct >> 5;
     const int grp = cw / TPRW, wis = cw - grp * TPRW, lr = ct - grp * TPR;
     epoch_read(sh, a.sync, ct);
-    Philox<MASK == kMaskRngState> gen;
-    if constexpr (RNG) gen.load(a.rng);
+    Philox<true> gen;
+    if constexpr (RNG) gen.load(a.rng, keys);
     const f2 scale2 = f2_splat(a.scale);
     const int gbar = 2 + grp;  // the group's named barrier
 
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
         f2 r2[NP];
         PK::get(rres, r2);
         if constexpr (RNG) {
-          rng_pairs<NP>(gen, a.rng, i0, keep2);
+          rng_pairs<NP>(gen, i0, keep2);
 #pragma unroll
           for (int p = 0; p < NP; ++p)
             z2[p] = a.zin ? x2[p]
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
         Vec<T, VE>::cvt(rres, rv);
         if constexpr (RNG) {
           bool f[VE];
-          gen.template keep<VE>(a.rng, i0, f);
+          gen.template keep<VE>(i0, f);
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
             const bool on = f[e];
@@ -672,10 +673,10 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
 // t, t+256, ...; column sums go straight into this block's partial rows.
 template <typename T, bool FUSED, int MASK>
 __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
-  constexpr bool RNG = MASK != kMaskBytes;
+  constexpr bool RNG = MASK == kMaskRng;
   extern __shared__ __align__(16) uint8_t gbits[];
   RowBits rb{a.H <= kRowBitsMaxH ? gbits : nullptr, 0};
-  PhiloxAny gen;
+  Philox<false> gen;
   if constexpr (RNG) gen.load(a.rng);
   constexpr bool COMP = sizeof(T) == 4;
   __shared__ float red[2][2][32];
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
     keep = 1.f;
     if constexpr (FUSED) {
       if constexpr (RNG)
-        keep = rowbits_keep(rb, gen, a.rng, (uint64_t)(r * H + j)) ? a.scale : 0.f;
+        keep = rowbits_keep(rb, gen, (uint64_t)(r * H + j)) ? a.scale : 0.f;
       else
         keep = (a.mask == nullptr || a.mask[r * H + j] != 0) ? a.scale : 0.f;
       if (a.zin) return z;
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(256) ln_bwd_generic_kernel(LnArgs a) {
   int it = 0;
   for (int64_t r = g; r < a.R; r += G, ++it) {
     const float mu = a.mean[r], rho = a.rstd[r];
-    if constexpr (RNG) rowbits_fill(rb, gen, a.rng, (uint64_t)(r * H), H);
+    if constexpr (RNG) rowbits_fill(rb, gen, (uint64_t)(r * H), H);
     float sg = 0.f, sgx = 0.f;
     for (int64_t j = tid; j < H; j += blockDim.x) {
       float keep;
@@ -811,11 +812,9 @@ cudaError_t launch_ring(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
 // (at most 8), the counts the plan uses.
 template <typename T, bool FUSED, int MASK = kMaskBytes>
 cudaError_t launch_typed(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
-  if (!p.fast) {
-    constexpr int M = MASK == kMaskBytes ? kMaskBytes : kMaskRng;  // any seed
-    return launch(ln_bwd_generic_kernel<T, FUSED, M>, dim3(p.G), dim3(p.threads),
-                  M == kMaskRng ? rowbits_bytes(a.H) : 0, st, false, a);
-  }
+  if (!p.fast)
+    return launch(ln_bwd_generic_kernel<T, FUSED, MASK>, dim3(p.G), dim3(p.threads),
+                  MASK == kMaskRng ? rowbits_bytes(a.H) : 0, st, false, a);
   if constexpr (sizeof(T) == 2)
     if (p.kv == 2) return launch_ring<T, 2, FUSED, MASK>(p, a, st);
   return launch_ring<T, 1, FUSED, MASK>(p, a, st);
@@ -829,12 +828,7 @@ cudaError_t set_smem(int bytes) {
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   cudaError_t e3 = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, true, kMaskRng, kLnRingWarps[KV]>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  cudaError_t e4 =
-      cudaFuncSetAttribute(ln_bwd_ring_kernel<T, KV, true, kMaskRngState, kLnRingWarps[KV]>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  for (cudaError_t e : {e1, e2, e3, e4})
-    if (e != cudaSuccess) return e;
-  return cudaSuccess;
+  return e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : e3);
 }
 
 template <typename T>
@@ -899,12 +893,8 @@ cudaError_t ln_launch(const RowPlan& p, const LnPtrs& q, void* ws, int* status,
   if (q.rng != nullptr) {
     a.rng = *q.rng;
     a.scale = q.rng->scale;
-    if (a.rng.state != nullptr)
-      e = p.dtype == GBN_F32 ? launch_typed<float, true, kMaskRngState>(p, a, st)
-                             : launch_typed<bf16, true, kMaskRngState>(p, a, st);
-    else
-      e = p.dtype == GBN_F32 ? launch_typed<float, true, kMaskRng>(p, a, st)
-                             : launch_typed<bf16, true, kMaskRng>(p, a, st);
+    e = p.dtype == GBN_F32 ? launch_typed<float, true, kMaskRng>(p, a, st)
+                           : launch_typed<bf16, true, kMaskRng>(p, a, st);
   } else if (p.dtype == GBN_F32)
     e = fused ? launch_typed<float, true>(p, a, st) : launch_typed<float, false>(p, a, st);
   else
