@@ -305,6 +305,7 @@ cudaError_t selftest_bounded_wait(int* status, uint64_t limit_ns, cudaStream_t s
 
 struct GnPlan {
   int64_t N = 0, S = 0, C = 0, G = 0;  // samples, rows per sample, channels, groups
+  bool backward = false;
   int vec = 1;              // channels per vector (divides C)
   int TX = 1, TY = 1;       // block shape: vectors x rows
   int tiles = 1;            // channel tiles of TX vectors
@@ -312,7 +313,6 @@ struct GnPlan {
   int threads = 32;         // block size
   int tile_groups = 1;      // groups a tile can touch, at most
   int rps = 1;              // rows per slice
-  int64_t run = 1;          // samples per pair of launches
   size_t gpart_bytes = 0;   // group partials; the channel partials follow
   size_t ws_bytes = 0;
 };

@@ -14,7 +14,7 @@
 // Layout of a block: TX threads over 16-byte (or narrower) vectors of adjacent
 // channels, TY thread rows down the block's slice of one sample's rows, so a
 // warp reads contiguous bytes and a thread's channels never change.  A block
-// covers a tile of at most 256 vectors; a group cut by a tile border simply has
+// covers a tile of at most 256 vectors and 1024 channels; a group cut by a tile border simply has
 // one partial in each tile (entry g + tile, unique because a border cuts at
 // most one group).
 //
@@ -36,6 +36,7 @@ namespace gbn {
 namespace {
 
 constexpr int kGThreads = 256;
+constexpr int kGnTogether = 2; // groups whose reductions overlap
 constexpr int kGnFewRows = 8;  // thread rows that one thread adds up per channel
 
 struct GnGeom {
@@ -47,10 +48,9 @@ struct GnGeom {
   int32_t slices;     // row slices per sample
   int32_t rps;        // rows per slice (the last may have fewer)
   int32_t E;          // group partials per (sample, slice): G + T - 1
-  int32_t n0;         // first sample of this launch
   int32_t cols, R;    // finalize: groups side by side, thread rows
   int32_t llc;        // log2 of the lanes over a group's channels
-  FastDiv dTX, dCg, dcols, dTY;
+  FastDiv dTX, dCg, dcols, dTY, dT;
 };
 
 struct GnArgs {
@@ -67,7 +67,7 @@ struct GnArgs {
   float eps, slope;
 };
 
-// Grid: (tile, slice, sample).
+// Grid: (sample and tile, slice).
 struct GnBlock {
   int n, slice, tile;
   int tx, ty;
@@ -82,11 +82,11 @@ struct GnBlock {
 };
 
 template <int VEC>
-__device__ __forceinline__ GnBlock gn_block(const GnGeom& g) {
+__device__ __forceinline__ GnBlock gn_block(const GnGeom& g, uint32_t item) {
   GnBlock b;
-  b.tile = blockIdx.x;
+  b.n = g.T == 1 ? (int)item : (int)fast_div(item, g.dT);
+  b.tile = item - b.n * g.T;
   b.slice = blockIdx.y;
-  b.n = g.n0 + (int)blockIdx.z;
   b.ty = fast_div(threadIdx.x, g.dTX);
   b.tx = threadIdx.x - b.ty * g.TX;
   b.cv = b.tile * g.TX + b.tx;
@@ -166,21 +166,6 @@ __device__ __forceinline__ f2 gn_gated(f2 d, f2 npre, float slope) {
   }
 }
 
-// ------------------------------------------------- merging of statistics --
-
-// (n, mean, M2) of a set of values.
-struct Mom {
-  float n, mean, M2;
-};
-__device__ __forceinline__ void mom_add(Mom& a, const Mom& b) {
-  const float n = a.n + b.n;
-  if (b.n == 0.f) return;
-  const float w = __fdividef(b.n, n), d = b.mean - a.mean;
-  a.M2 = fmaf(d * d, a.n * w, a.M2 + b.M2);
-  a.mean = fmaf(d, w, a.mean);
-  a.n = n;
-}
-
 // ---------------------------------------------------------- statistics --
 
 template <typename T, int VEC>
@@ -190,9 +175,9 @@ __global__ void __launch_bounds__(kGThreads, 3) gn_stats_kernel(const GnArgs a) 
   using V = Vec<T, VEC>;
   __shared__ float2 acc[kGThreads * VEC];  // [ty][channel of the tile]: mean - K, M2
   __shared__ float Ks[kGThreads * VEC];    // shifts: x[n, 0, c]
-  const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g);
   pdl_launch_dependents();
+  const GnGeom& g = a.g;
+  const GnBlock b = gn_block<VEC>(g, blockIdx.x);
   const T* xs = static_cast<const T*>(a.x) + (int64_t)b.n * g.S * g.C;
   const int W = g.TX * VEC;  // channels of a full tile
   if (b.active) {
@@ -273,65 +258,108 @@ __global__ void __launch_bounds__(kGThreads, 3) gn_stats_kernel(const GnArgs a) 
     if (b.slice == 0 && gi * g.Cg >= b.c0) a.cpart[(int64_t)b.n * g.G + gi] = K0;
   };
   if (g.TY <= kGnFewRows) {
-    // a thread per channel over the thread rows, then teams of lanes over the
-    // channels of a group
+    // a thread per channel over the thread rows (all reads in flight), then
+    // teams of lanes over the channels of a group, kGnTogether groups at a time
     const float inv = __fdividef(1.f, (float)b.rows);
     for (int c = threadIdx.x; c < b.c1 - b.c0; c += blockDim.x) {
+      float2 v[kGnFewRows];
+#pragma unroll
+      for (int ty = 0; ty < kGnFewRows; ++ty)
+        v[ty] = ty < g.TY ? acc[ty * W + c] : make_float2(0.f, 0.f);
       float s = 0.f, q = 0.f;
-      for (int ty = 0; ty < g.TY; ++ty) s = fmaf(weight(ty), acc[ty * W + c].x, s);
+#pragma unroll
+      for (int ty = 0; ty < kGnFewRows; ++ty)
+        if (ty < g.TY) s = fmaf(weight(ty), v[ty].x, s);
       const float mean = s * inv;
-      for (int ty = 0; ty < g.TY; ++ty) {
-        const float2 v = acc[ty * W + c];
-        const float d = v.x - mean;
-        q += fmaf(weight(ty) * d, d, v.y);
-      }
+#pragma unroll
+      for (int ty = 0; ty < kGnFewRows; ++ty)
+        if (ty < g.TY) {
+          const float d = v[ty].x - mean;
+          q += fmaf(weight(ty) * d, d, v[ty].y);
+        }
       acc[c] = make_float2(mean, q);  // row 0 of the channel: only this thread reads it
     }
     __syncthreads();
     const int L = 1 << g.llc, l = lane & (L - 1), teams = blockDim.x >> g.llc;
-    for (int gb = b.g0; gb < b.g1; gb += teams) {
-      const int gi = gb + (threadIdx.x >> g.llc);
-      const bool on = gi < b.g1;
-      const int ca = on ? max(gi * g.Cg, b.c0) - b.c0 : 0;
-      const int cb = on ? min((gi + 1) * g.Cg, b.c1) - b.c0 : 0;
-      const float Kg = Ks[ca];
-      float s = 0.f, q = 0.f;
-      for (int c = ca + l; c < cb; c += L) s += (Ks[c] - Kg) + acc[c].x;
-      for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float mean = __fdividef(s, (float)(cb - ca));
-      for (int c = ca + l; c < cb; c += L) {
-        const float2 v = acc[c];
-        const float d = ((Ks[c] - Kg) + v.x) - mean;
-        q += fmaf((float)b.rows * d, d, v.y);
+    for (int gb = b.g0; gb < b.g1; gb += teams * kGnTogether) {
+      int ca[kGnTogether], cb[kGnTogether];
+      float Kg[kGnTogether], s[kGnTogether], q[kGnTogether];
+#pragma unroll
+      for (int r = 0; r < kGnTogether; ++r) {
+        const int gi = gb + r * teams + (threadIdx.x >> g.llc);
+        const bool on = gi < b.g1;
+        ca[r] = on ? max(gi * g.Cg, b.c0) - b.c0 : 0;
+        cb[r] = on ? min((gi + 1) * g.Cg, b.c1) - b.c0 : 0;
+        Kg[r] = Ks[ca[r]];
+        s[r] = q[r] = 0.f;
+        for (int c = ca[r] + l; c < cb[r]; c += L) s[r] += (Ks[c] - Kg[r]) + acc[c].x;
       }
-      for (int o = L / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-      if (on && l == 0) write(gi, Kg, mean, q);
-    }
-  } else {
-    // few channels, many thread rows: a warp per group, lanes over both
-    const int Lc = 1 << g.llc, lc = lane & (Lc - 1), lt = lane >> g.llc, Lt = 32 >> g.llc;
-    for (int gi = b.g0 + warp; gi < b.g1; gi += nw) {
-      const int ca = max(gi * g.Cg, b.c0) - b.c0, cb = min((gi + 1) * g.Cg, b.c1) - b.c0;
-      const float Kg = Ks[ca];
-      float s = 0.f, q = 0.f;
-      for (int c = ca + lc; c < cb; c += Lc) {
-        const float dk = Ks[c] - Kg;
-        for (int ty = lt; ty < g.TY; ty += Lt) s = fmaf(weight(ty), dk + acc[ty * W + c].x, s);
-      }
-      const float mean = __fdividef(warp_sum(s), (float)b.rows * (float)(cb - ca));
-      for (int c = ca + lc; c < cb; c += Lc) {
-        const float dk = (Ks[c] - Kg) - mean;
-        for (int ty = lt; ty < g.TY; ty += Lt) {
-          const float2 v = acc[ty * W + c];
-          const float d = dk + v.x;
-          q += fmaf(weight(ty) * d, d, v.y);
+      for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < kGnTogether; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+#pragma unroll
+      for (int r = 0; r < kGnTogether; ++r) {
+        s[r] = __fdividef(s[r], (float)(cb[r] - ca[r]));
+        for (int c = ca[r] + l; c < cb[r]; c += L) {
+          const float2 v = acc[c];
+          const float d = ((Ks[c] - Kg[r]) + v.x) - s[r];
+          q[r] += fmaf((float)b.rows * d, d, v.y);
         }
       }
-      q = warp_sum(q);
-      if (lane == 0) write(gi, Kg, mean, q);
+      for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < kGnTogether; ++r) q[r] += __shfl_xor_sync(0xffffffffu, q[r], o);
+#pragma unroll
+      for (int r = 0; r < kGnTogether; ++r)
+        if (cb[r] > ca[r] && l == 0)
+          write(gb + r * teams + (threadIdx.x >> g.llc), Kg[r], s[r], q[r]);
+    }
+  } else {
+    // few channels, many thread rows: a warp per group, lanes over both,
+    // kGnTogether groups at a time
+    const int Lc = 1 << g.llc, lc = lane & (Lc - 1), lt = lane >> g.llc, Lt = 32 >> g.llc;
+    for (int gb = b.g0 + warp; gb < b.g1; gb += nw * kGnTogether) {
+      int ca[kGnTogether], cb[kGnTogether];
+      float Kg[kGnTogether], s[kGnTogether], q[kGnTogether];
+#pragma unroll
+      for (int r = 0; r < kGnTogether; ++r) {
+        const int gi = gb + r * nw;
+        const bool on = gi < b.g1;
+        ca[r] = on ? max(gi * g.Cg, b.c0) - b.c0 : 0;
+        cb[r] = on ? min((gi + 1) * g.Cg, b.c1) - b.c0 : 0;
+        Kg[r] = Ks[ca[r]];
+        s[r] = q[r] = 0.f;
+        for (int c = ca[r] + lc; c < cb[r]; c += Lc) {
+          const float dk = Ks[c] - Kg[r];
+          for (int ty = lt; ty < g.TY; ty += Lt)
+            s[r] = fmaf(weight(ty), dk + acc[ty * W + c].x, s[r]);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < kGnTogether; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+#pragma unroll
+      for (int r = 0; r < kGnTogether; ++r) {
+        s[r] = __fdividef(s[r], (float)b.rows * (float)(cb[r] - ca[r]));
+        for (int c = ca[r] + lc; c < cb[r]; c += Lc) {
+          const float dk = (Ks[c] - Kg[r]) - s[r];
+          for (int ty = lt; ty < g.TY; ty += Lt) {
+            const float2 v = acc[ty * W + c];
+            const float d = dk + v.x;
+            q[r] += fmaf(weight(ty) * d, d, v.y);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < kGnTogether; ++r) q[r] += __shfl_xor_sync(0xffffffffu, q[r], o);
+#pragma unroll
+      for (int r = 0; r < kGnTogether; ++r)
+        if (cb[r] > ca[r] && lane == 0) write(gb + r * nw, Kg[r], s[r], q[r]);
     }
   }
-  pdl_wait();  // the previous launch of this call (another run of samples) is complete too
 }
 
 // Tiles that hold channels of group gi: first and one past the last.
@@ -346,45 +374,72 @@ __device__ __forceinline__ void gn_tiles_of(const GnGeom& g, int gi, int& t0, in
   t1 = (int)fast_div(((gi + 1) * g.Cg - 1) / VEC, g.dTX) + 1;
 }
 
-// Walks the partials of the tile's groups: thread row q of R takes slices q,
-// q + R, ... of group gi = g0 + column, `take(partial, rows, channels)` per
-// partial; `done(gi, q, R, on)` is called by every thread between barriers'
-// needs (on: the thread has a group).  Groups beyond the block's width come in
-// further rounds.
-template <int VEC, typename Init, typename Take, typename Done>
-__device__ __forceinline__ void gn_walk(const GnArgs& a, const GnBlock& b, Init init, Take take,
-                                        Done done) {
+// Sums over the partials of the tile's groups: thread row q of R takes slices q,
+// q + R, ... of group g0 + column (all its reads in flight), `take(acc, partial,
+// rows, channels)` adds one to the NV sums, which then meet in shared memory
+// (`red`, NV arrays of the block's size); `done(gi, sums)` runs once per group.
+// Groups beyond the block's width come in further rounds.  Barriers inside.
+template <int VEC, int NV, typename Begin, typename Take, typename Done>
+__device__ __forceinline__ void gn_walk(const GnArgs& a, const GnBlock& b, float* red, Begin begin,
+                                        Take take, Done done) {
   const GnGeom& g = a.g;
-  const int cols = g.cols, R = g.R;
+  const int cols = g.cols;
   const int q = (int)fast_div(threadIdx.x, g.dcols), col = threadIdx.x - q * cols;
   for (int gb = b.g0; gb < b.g1; gb += cols) {
     const int gi = gb + col;
-    const bool on = q < R && gi < b.g1;
-    init();
+    const bool on = q < g.R && gi < b.g1;
+    float acc[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) acc[k] = 0.f;
     if (on) {
       int t0, t1;
       gn_tiles_of<VEC>(g, gi, t0, t1);
       const int W = g.TX * VEC;
       const float2* part = a.gpart + (int64_t)b.n * g.slices * g.E + gi;
+      begin(part + (int64_t)(g.slices / 2) * g.E + t0);
       for (int t = t0; t < t1; ++t) {
         const float ch = g.T == 1 ? (float)g.Cg
                                   : (float)(min((gi + 1) * g.Cg, (t + 1) * W) - max(gi * g.Cg, t * W));
         constexpr int U = 8;
-        for (int j = q; j < g.slices; j += U * R) {
+        for (int j = q; j < g.slices; j += U * g.R) {
           float2 v[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (j + u * R < g.slices) v[u] = __ldcg(part + (int64_t)(j + u * R) * g.E + t);
+          for (int u = 0; u < U; ++u) {
+            v[u] = make_float2(0.f, 0.f);
+            if (j + u * g.R < g.slices) v[u] = __ldcg(part + (int64_t)(j + u * g.R) * g.E + t);
+          }
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            if (j + u * R < g.slices) {
-              const int rows = min(g.rps, g.S - (j + u * R) * g.rps);
-              take(v[u], (float)rows, ch);
-            }
+            if (j + u * g.R < g.slices)
+              take(acc, v[u], (float)min(g.rps, g.S - (j + u * g.R) * g.rps), ch);
         }
       }
     }
-    done(gi, q, R, col, cols, on);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) red[k * kGThreads + threadIdx.x] = acc[k];
+    __syncthreads();
+    int R = g.R;
+    while (R > 8) {  // halve the thread rows, then one thread adds up to eight
+      const int h = (R + 1) / 2;
+      if (on && q + h < R) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          red[k * kGThreads + threadIdx.x] += red[k * kGThreads + threadIdx.x + h * cols];
+      }
+      R = h;
+      __syncthreads();
+    }
+    if (on && q == 0) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = r < R ? red[k * kGThreads + r * cols + col] : 0.f;
+        acc[k] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      }
+      done(gi, acc);
+    }
+    __syncthreads();
   }
 }
 
@@ -403,16 +458,20 @@ __device__ __forceinline__ void gn_const(const float* arr, int tx, f2 (&p)[kPair
   for (int k = 0; k < kPairs<VEC>; ++k) p[k] = pair_at(v, k);
 }
 
+// The second passes take the samples from the last, and every slice from its
+// end: what the first pass read last is likeliest in L2.
+__device__ __forceinline__ uint32_t gn_from_last() { return gridDim.x - 1 - blockIdx.x; }
+
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_apply_kernel(const GnArgs a) {
   constexpr int U = 4;
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   extern __shared__ float3 fin[];  // per group of the tile: mean hi, lo, rstd
-  __shared__ Mom red[kGThreads];
-  __shared__ __align__(16) float cst[3][kGThreads * VEC];  // per channel: mean hi, scale, shift
+  __shared__ __align__(16) float cst[3][kGThreads * VEC];  // mean hi, -scale, -shift
+  __shared__ float red[2 * kGThreads];
   const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g);
+  const GnBlock b = gn_block<VEC>(g, gn_from_last());
   const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
   const T* xs = static_cast<const T*>(a.x) + base;
   T* ys = static_cast<T*>(a.out) + base;
@@ -433,37 +492,29 @@ __global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_apply_kernel(co
   };
   load();
   pdl_wait();
-  pdl_launch_dependents();
-  Mom m{0.f, 0.f, 0.f};
-  gn_walk<VEC>(
-      a, b, [&] { m = Mom{0.f, 0.f, 0.f}; },
-      [&](float2 v, float rows, float ch) { mom_add(m, Mom{rows * ch, v.x, v.y}); },
-      [&](int gi, int q, int R, int col, int cols, bool on) {
-        red[threadIdx.x] = m;
-        __syncthreads();
-        int P = 1;
-        while (P < R) P *= 2;
-        for (int step = P / 2; step >= 1; step /= 2) {
-          if (on && q < step && q + step < R) {
-            Mom t = red[q * cols + col];
-            mom_add(t, red[(q + step) * cols + col]);
-            red[q * cols + col] = t;
-          }
-          __syncthreads();
+  // Sums relative to the middle slice's mean m0, which is one of the summands:
+  // sum n (m - m0)^2 exceeds the spread between the slices at most slices-fold,
+  // so the final difference is safe.
+  float m0 = 0.f;
+  gn_walk<VEC, 2>(
+      a, b, red, [&](const float2* mid) { m0 = __ldcg(mid).x; },
+      [&](float(&acc)[2], float2 v, float rows, float ch) {
+        const float d = v.x - m0, nd = (rows * ch) * d;
+        acc[0] += nd;
+        acc[1] += fmaf(nd, d, v.y);
+      },
+      [&](int gi, float(&acc)[2]) {
+        const float cnt = (float)g.S * (float)g.Cg, dm = acc[0] / cnt;
+        const float var = fmaxf(fmaf(-acc[0], dm, acc[1]), 0.f) / cnt;
+        const DF mu = two_sum(__ldcg(a.cpart + (int64_t)b.n * g.G + gi), m0 + dm);
+        const float rstd = rsqrtf(var + a.eps);
+        fin[gi - b.g0] = make_float3(mu.hi, mu.lo, rstd);
+        if (b.slice == 0 && gi * g.Cg >= b.c0) {
+          const int64_t o = (int64_t)b.n * g.G + gi, ng = (int64_t)g.N * g.G;
+          a.stats[o] = mu.hi;
+          a.stats[ng + o] = rstd;
+          a.stats[2 * ng + o] = mu.lo;
         }
-        if (on && q == 0) {
-          const Mom t = red[col];
-          const DF mu = two_sum(__ldcg(a.cpart + (int64_t)b.n * g.G + gi), t.mean);
-          const float rstd = 1.f / sqrtf(t.M2 / t.n + a.eps);
-          fin[gi - b.g0] = make_float3(mu.hi, mu.lo, rstd);
-          if (b.slice == 0 && gi * g.Cg >= b.c0) {
-            const int64_t o = (int64_t)b.n * g.G + gi, ng = (int64_t)g.N * g.G;
-            a.stats[o] = mu.hi;
-            a.stats[ng + o] = rstd;
-            a.stats[2 * ng + o] = mu.lo;
-          }
-        }
-        __syncthreads();
       });
   for (int k = threadIdx.x; k < b.c1 - b.c0; k += blockDim.x) {
     const int c = b.c0 + k;
@@ -514,22 +565,44 @@ template <typename T> struct GnSum {
 // Per channel of the tile: sum e and sum e*xhat of the block's rows, to the
 // column partials; and per group the sums of gamma*e and gamma*e*xhat.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_sums_kernel(const GnArgs a) {
+__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
+    gn_sums_kernel(const GnArgs a) {
   constexpr int U = 4;  // rows in flight (two inputs)
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   __shared__ __align__(16) DF sab[2][kGThreads * VEC];  // [ty][channel]
   DF* sa = sab[0];
   DF* sb = sab[1];
-  const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g);
   pdl_launch_dependents();
+  const GnGeom& g = a.g;
+  const GnBlock b = gn_block<VEC>(g, blockIdx.x);
   const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
   const T* xs = static_cast<const T*>(a.x) + base;
   const T* ds = static_cast<const T*>(a.dy) + base;
   const int W = g.TX * VEC;
   const int64_t ng = (int64_t)g.N * g.G, so = (int64_t)b.n * g.G;
-  float* cst = reinterpret_cast<float*>(sa);  // per channel: mean hi, scale, shift
+  // the first rows are on their way while the constants are formed
+  uint32_t o = b.off;
+  int left = b.active ? b.left : 0;
+  typename V::raw rx[U], rd[U];
+  auto load = [&] {
+    if (left >= U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rx[u] = V::ld(xs + (o + u * b.step));
+        rd[u] = V::ld(ds + (o + u * b.step));
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U - 1; ++u)
+        if (u < left) {
+          rx[u] = V::ld(xs + (o + u * b.step));
+          rd[u] = V::ld(ds + (o + u * b.step));
+        }
+    }
+  };
+  load();
+  float* cst = reinterpret_cast<float*>(sa);  // per channel: mean hi, -scale, -shift
   for (int k = threadIdx.x; k < b.c1 - b.c0; k += blockDim.x) {
     const int c = b.c0 + k, gi = fast_div(c, g.dCg);
     const float s1 = a.stats[ng + so + gi] * (a.gamma ? a.gamma[c] : 1.f);
@@ -545,13 +618,11 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_sum
   __syncthreads();  // the sums below reuse the memory
   if (b.active) {
     GnSum<T> A[NP], B[NP];
-    uint32_t o = b.off;
-    int left = b.left;
     f2 ca[NP], cb[NP];
-    auto row = [&](typename V::raw rx, typename V::raw rd) {
+    auto row = [&](int u) {
       f2 v[NP], d[NP];
-      to_pairs<T, VEC>(rx, v);
-      to_pairs<T, VEC>(rd, d);
+      to_pairs<T, VEC>(rx[u], v);
+      to_pairs<T, VEC>(rd[u], d);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const f2 xc = f2_sub(v[k], nm[k]);
@@ -560,42 +631,28 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_sum
         cb[k] = f2_fma(t, xc, cb[k]);
       }
     };
-    for (; left >= U; left -= U, o += U * b.step) {
-      typename V::raw rx[U], rd[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        rx[u] = V::ld(xs + (o + u * b.step));
-        rd[u] = V::ld(ds + (o + u * b.step));
-      }
-#pragma unroll
-      for (int k = 0; k < NP; ++k) ca[k] = cb[k] = 0ull;
-#pragma unroll
-      for (int u = 0; u < U; ++u) row(rx[u], rd[u]);
+    auto flush = [&] {
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         A[k].add(ca[k]);
         B[k].add(cb[k]);
+        ca[k] = cb[k] = 0ull;
       }
+    };
+#pragma unroll
+    for (int k = 0; k < NP; ++k) ca[k] = cb[k] = 0ull;
+    while (left >= U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) row(u);
+      flush();
+      left -= U;
+      o += U * b.step;
+      load();
     }
-    if (left > 0) {
-      typename V::raw rx[U - 1], rd[U - 1];
 #pragma unroll
-      for (int u = 0; u < U - 1; ++u)
-        if (u < left) {
-          rx[u] = V::ld(xs + (o + u * b.step));
-          rd[u] = V::ld(ds + (o + u * b.step));
-        }
-#pragma unroll
-      for (int k = 0; k < NP; ++k) ca[k] = cb[k] = 0ull;
-#pragma unroll
-      for (int u = 0; u < U - 1; ++u)
-        if (u < left) row(rx[u], rd[u]);
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        A[k].add(ca[k]);
-        B[k].add(cb[k]);
-      }
-    }
+    for (int u = 0; u < U - 1; ++u)
+      if (u < left) row(u);
+    flush();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const int i = b.ty * W + b.tx * VEC + e;
@@ -651,7 +708,6 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_sum
     }
     if (on && lane == 0) a.gpart[row * g.E + gi + b.tile] = make_float2(s, q);
   }
-  pdl_wait();  // the previous launch of this call (another run of samples) is complete too
 }
 
 // ------------------------------------------------------- weight gradients --
@@ -719,15 +775,16 @@ __global__ void __cluster_dims__(kGnWCluster, 1, 1) __launch_bounds__(1024)
 // ------------------------------------------------------------------- dx --
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_dx_kernel(const GnArgs a) {
+__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
+    gn_dx_kernel(const GnArgs a) {
   constexpr int U = 4;
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
-  extern __shared__ float2 kk[];  // per group of the tile: k0, k1
-  __shared__ float2 red[kGThreads];
+  extern __shared__ float2 kk[];  // k0, k1 of the tile's groups
   __shared__ __align__(16) float cst[6][kGThreads * VEC];  // per channel
+  __shared__ float red[2 * kGThreads];
   const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g);
+  const GnBlock b = gn_block<VEC>(g, gn_from_last());
   const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
   const T* xs = static_cast<const T*>(a.x) + base;
   const T* ds = static_cast<const T*>(a.dy) + base;
@@ -756,30 +813,15 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_dx_
   load();
   pdl_wait();
   pdl_launch_dependents();
-  float2 m = make_float2(0.f, 0.f);
-  gn_walk<VEC>(
-      a, b, [&] { m = make_float2(0.f, 0.f); },
-      [&](float2 v, float, float) {
-        m.x += v.x;
-        m.y += v.y;
+  gn_walk<VEC, 2>(
+      a, b, red, [](const float2*) {},
+      [](float(&acc)[2], float2 v, float, float) {
+        acc[0] += v.x;
+        acc[1] += v.y;
       },
-      [&](int gi, int q, int R, int col, int cols, bool on) {
-        red[threadIdx.x] = m;
-        __syncthreads();
-        int P = 1;
-        while (P < R) P *= 2;
-        for (int step = P / 2; step >= 1; step /= 2) {
-          if (on && q < step && q + step < R) {
-            const float2 u = red[q * cols + col], v = red[(q + step) * cols + col];
-            red[q * cols + col] = make_float2(u.x + v.x, u.y + v.y);
-          }
-          __syncthreads();
-        }
-        if (on && q == 0) {
-          const float inv = 1.f / ((float)g.S * (float)g.Cg);
-          kk[gi - b.g0] = make_float2(red[col].x * inv, red[col].y * inv);
-        }
-        __syncthreads();
+      [&](int gi, float(&acc)[2]) {
+        const float inv = 1.f / ((float)g.S * (float)g.Cg);
+        kk[gi - b.g0] = make_float2(acc[0] * inv, acc[1] * inv);
       });
   // dx = sc*e + (x - mean_hi)*q1 + q0
   for (int k = threadIdx.x; k < b.c1 - b.c0; k += blockDim.x) {
@@ -829,48 +871,46 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4) gn_dx_
 
 // ----------------------------------------------------------------- host --
 
-enum GnKernel { kGnStats, kGnApply, kGnSums, kGnDx };
-
+// Both passes of a direction.
 template <typename T, int VEC, int ACT>
-cudaError_t gn_run(GnKernel k, const GnPlan& p, const GnArgs& a, cudaStream_t st) {
-  const bool chained = a.g.n0 > 0;  // not the call's first launch
-  const int64_t n = p.N - a.g.n0 < p.run ? p.N - a.g.n0 : p.run;
-  const dim3 grid((unsigned)p.tiles, (unsigned)p.slices, (unsigned)n);
+cudaError_t gn_run(const GnPlan& p, const GnArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)(p.N * p.tiles), (unsigned)p.slices);
   const dim3 block((unsigned)p.threads);
-  const size_t smem = (size_t)p.tile_groups;
-  if (k == kGnStats) return launch(gn_stats_kernel<T, VEC>, grid, block, 0, st, chained, a);
-  if (k == kGnApply)
-    return launch(gn_apply_kernel<T, VEC, ACT>, grid, block, smem * sizeof(float3), st, true, a);
+  const size_t groups = (size_t)p.tile_groups;
+  if (!p.backward) {
+    const cudaError_t e = launch(gn_stats_kernel<T, VEC>, grid, block, 0, st, false, a);
+    if (e != cudaSuccess) return e;
+    return launch(gn_apply_kernel<T, VEC, ACT>, grid, block, groups * sizeof(float3), st, true, a);
+  }
   if constexpr (VEC <= 4) {  // the backward's widest (gn_plan)
-    if (k == kGnSums)
-      return launch(gn_sums_kernel<T, VEC, ACT>, grid, block, 0, st, chained, a);
-    return launch(gn_dx_kernel<T, VEC, ACT>, grid, block, smem * sizeof(float2), st, true, a);
+    const cudaError_t e = launch(gn_sums_kernel<T, VEC, ACT>, grid, block, 0, st, false, a);
+    if (e != cudaSuccess) return e;
+    return launch(gn_dx_kernel<T, VEC, ACT>, grid, block, groups * sizeof(float2), st, true, a);
   }
   return cudaErrorInvalidValue;
 }
 template <typename T, int VEC>
-cudaError_t gn_run_act(GnKernel k, int act, const GnPlan& p, const GnArgs& a, cudaStream_t st) {
+cudaError_t gn_run_act(int act, const GnPlan& p, const GnArgs& a, cudaStream_t st) {
   switch (act) {
-    case GBN_ACT_RELU: return gn_run<T, VEC, GBN_ACT_RELU>(k, p, a, st);
-    case GBN_ACT_LEAKY_RELU: return gn_run<T, VEC, GBN_ACT_LEAKY_RELU>(k, p, a, st);
-    case GBN_ACT_SILU: return gn_run<T, VEC, GBN_ACT_SILU>(k, p, a, st);
-    default: return gn_run<T, VEC, GBN_ACT_NONE>(k, p, a, st);
+    case GBN_ACT_RELU: return gn_run<T, VEC, GBN_ACT_RELU>(p, a, st);
+    case GBN_ACT_LEAKY_RELU: return gn_run<T, VEC, GBN_ACT_LEAKY_RELU>(p, a, st);
+    case GBN_ACT_SILU: return gn_run<T, VEC, GBN_ACT_SILU>(p, a, st);
+    default: return gn_run<T, VEC, GBN_ACT_NONE>(p, a, st);
   }
 }
-cudaError_t gn_dispatch(GnKernel k, int dtype, int act, const GnPlan& p, const GnArgs& a,
-                        cudaStream_t st) {
+cudaError_t gn_dispatch(int dtype, int act, const GnPlan& p, const GnArgs& a, cudaStream_t st) {
   if (dtype == GBN_F32) {
     switch (p.vec) {
-      case 4: return gn_run_act<float, 4>(k, act, p, a, st);
-      case 2: return gn_run_act<float, 2>(k, act, p, a, st);
-      default: return gn_run_act<float, 1>(k, act, p, a, st);
+      case 4: return gn_run_act<float, 4>(act, p, a, st);
+      case 2: return gn_run_act<float, 2>(act, p, a, st);
+      default: return gn_run_act<float, 1>(act, p, a, st);
     }
   }
   switch (p.vec) {
-    case 8: return gn_run_act<bf16, 8>(k, act, p, a, st);
-    case 4: return gn_run_act<bf16, 4>(k, act, p, a, st);
-    case 2: return gn_run_act<bf16, 2>(k, act, p, a, st);
-    default: return gn_run_act<bf16, 1>(k, act, p, a, st);
+    case 8: return gn_run_act<bf16, 8>(act, p, a, st);
+    case 4: return gn_run_act<bf16, 4>(act, p, a, st);
+    case 2: return gn_run_act<bf16, 2>(act, p, a, st);
+    default: return gn_run_act<bf16, 1>(act, p, a, st);
   }
 }
 
@@ -893,6 +933,7 @@ GnArgs gn_args(const GnPlan& p, void* ws) {
   while (a.g.llc < 5 && (1 << a.g.llc) < a.g.Cg) ++a.g.llc;
   a.g.dTX = make_fast_div((uint32_t)p.TX);
   a.g.dTY = make_fast_div((uint32_t)p.TY);
+  a.g.dT = make_fast_div((uint32_t)p.tiles);
   a.g.dCg = make_fast_div((uint32_t)a.g.Cg);
   a.g.dcols = make_fast_div((uint32_t)a.g.cols);
   a.gpart = static_cast<float2*>(ws);
@@ -910,8 +951,11 @@ bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, int64_t esize,
   p->C = C;
   p->G = G;
   p->vec = vec;
+  p->backward = backward;
   const int64_t Cv = C / vec;
-  p->tiles = (int)((Cv + kGThreads - 1) / kGThreads);
+  // at most 1024 channels a tile: its constants and groups fit 48 KB
+  const int64_t max_tx = vec > 4 ? 1024 / vec : kGThreads;
+  p->tiles = (int)((Cv + max_tx - 1) / max_tx);
   p->TX = (int)((Cv + p->tiles - 1) / p->tiles);
   p->tiles = (int)((Cv + p->TX - 1) / p->TX);
   p->TY = kGThreads / p->TX;
@@ -920,19 +964,9 @@ bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, int64_t esize,
   const int64_t W = (int64_t)p->TX * vec, Cg = C / G;
   p->tile_groups = (int)((W + Cg - 1) / Cg + 1);  // cut at both ends
   if (p->tile_groups > G) p->tile_groups = (int)G;
-  // Samples per pair of launches: runs whose inputs stay in half of L2 between
-  // the two passes, so the second one reads no DRAM.
-  const int64_t sample = S * C * esize * (backward ? 2 : 1);
-  int64_t run = (int64_t)dev.l2_bytes / 2 / (sample > 0 ? sample : 1);
-  if (run < 1) run = 1;
-  if (run > N) run = N;
-  if (run > 65535) run = 65535;  // grid z
-  run = (N + (N + run - 1) / run - 1) / ((N + run - 1) / run);  // even runs
-  p->run = run;
-  // the resident block slots once over a run's samples, at least one round of
-  // loads a thread
+  // the resident block slots once, at least one round of loads a thread
   const int64_t slots = (int64_t)dev.sms * (backward && esize * vec <= 8 ? 4 : 3);
-  const int64_t per = slots / (run * p->tiles);
+  const int64_t per = slots / (N * p->tiles);
   const int64_t round = (int64_t)p->TY * 4;
   const int64_t rounds = (S + round - 1) / round;
   int64_t s = per < rounds ? per : rounds;
@@ -944,7 +978,7 @@ bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, int64_t esize,
   while ((int64_t)p->rps * C * esize > ((int64_t)1 << 31) && p->rps > 1) --p->rps;
   s = (S + p->rps - 1) / p->rps;
   p->slices = (int)s;
-  if (s > 65535) return false;
+  if (s > 65535 || N * p->tiles > INT32_MAX) return false;  // grid y, x
   p->gpart_bytes = ((size_t)N * s * (G + p->tiles - 1) * sizeof(float2) + 255) & ~(size_t)255;
   const size_t rest = backward ? (size_t)2 * N * s * C : (size_t)N * G;
   p->ws_bytes = p->gpart_bytes + ((rest * sizeof(float) + 255) & ~(size_t)255);
@@ -974,13 +1008,7 @@ cudaError_t gn_forward(const GnPlan& p, int dtype, const void* x, const float* g
   a.stats = stats;
   a.eps = eps;
   a.slope = slope;
-  cudaError_t e = cudaSuccess;
-  for (int64_t n = 0; n < p.N && e == cudaSuccess; n += p.run) {
-    a.g.n0 = (int32_t)n;
-    e = gn_dispatch(kGnStats, dtype, GBN_ACT_NONE, p, a, st);
-    if (e == cudaSuccess) e = gn_dispatch(kGnApply, dtype, act, p, a, st);
-  }
-  return e;
+  return gn_dispatch(dtype, act, p, a, st);
 }
 
 cudaError_t gn_backward(const GnPlan& p, int dtype, const void* x, const void* dy,
@@ -995,12 +1023,7 @@ cudaError_t gn_backward(const GnPlan& p, int dtype, const void* x, const void* d
   a.beta = beta;
   a.stats = const_cast<float*>(stats);
   a.slope = slope;
-  cudaError_t e = cudaSuccess;
-  for (int64_t n = 0; n < p.N && e == cudaSuccess; n += p.run) {
-    a.g.n0 = (int32_t)n;
-    e = gn_dispatch(kGnSums, dtype, act, p, a, st);
-    if (e == cudaSuccess) e = gn_dispatch(kGnDx, dtype, act, p, a, st);
-  }
+  const cudaError_t e = gn_dispatch(dtype, act, p, a, st);
   if (e != cudaSuccess || (dgamma == nullptr && dbeta == nullptr)) return e;
   const float* part = a.cpart;
   return launch(gn_weight_kernel, dim3((unsigned)((p.C + 31) / 32 * kGnWCluster)), dim3(1024), 0, st,

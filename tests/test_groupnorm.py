@@ -161,7 +161,7 @@ SHAPES = [  # N, spatial..., C, G
     ((1, 8, 8, 64), 32), ((2, 7, 5, 320), 32), ((3, 41, 10, 37), 1), ((1, 1, 2), 1),
     ((2, 3, 3, 1), 1), ((4, 1, 1, 48), 8), ((1, 30, 6, 4104), 3), ((2, 9, 2080), 4),
     ((1, 300, 12), 12), ((5, 17, 8), 2), ((1, 1000, 4), 1), ((2, 50, 6), 3), ((70, 2, 24), 4),
-    ((1, 5, 2049), 1), ((2, 64, 16), 16),
+    ((1, 5, 2049), 1), ((2, 64, 16), 16), ((1, 20, 2048), 2048), ((2, 3, 2056), 1028), ((70001, 1, 8), 2),
 ]
 
 
@@ -195,6 +195,16 @@ def test_more_shapes_and_options(gbn, dev, dtype):
     x, dy, gamma, beta = _inputs((2, 64, 64, 320), dtype, 8)       # many slices
     a = _check(gbn, x, dy, gamma, beta, 32, dtype, "silu", "many slices")
     b = _check(gbn, x, dy, gamma, beta, 32, dtype, "silu", "many slices")
+    # many runs of samples (more than L2 holds): every sample as it is alone
+    big = x.repeat(20, 1, 1, 1)
+    y, st = gbn.gn_nhwc_forward_train(big, 32, gamma, beta, act="silu")
+    dxb, dgb, dbb = gbn.gn_nhwc_backward(big, dy.repeat(20, 1, 1, 1), st, gamma, beta, act="silu")
+    assert torch.equal(y[:2], y[38:]) and torch.equal(dxb[:2], dxb[38:])
+    tol.check(y[6:8], _f64(a[0]), "runs y", dtype)
+    tol.check(dxb[6:8], _f64(a[2]), "runs dx", dtype)
+    torch.testing.assert_close(dgb / 20, a[3], rtol=2e-5, atol=2e-4)
+    torch.testing.assert_close(dbb / 20, a[4], rtol=2e-5, atol=2e-4)
+    del big, y, dxb
     assert all(torch.equal(p, q) for p, q in zip(a, b))
     z = x.clone()
     assert torch.equal(gbn.gn_nhwc_forward_train(z, 32, gamma, beta, act="silu", y=z)[0], a[0])
