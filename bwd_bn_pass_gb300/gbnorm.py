@@ -171,14 +171,20 @@ def _call(device, name, *args):
     """Call an entry point whose last argument is the stream, with ``device``
     current; raise on a nonzero status.  (The current device is switched only
     where it is another one: the switch costs more than a small kernel.)"""
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(device))
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, _stream(device))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != GBN_OK:
         raise GbnError(name, st)
+
+
+_entry = {}  # entry points by name
 
 
 @functools.lru_cache(maxsize=4096)
@@ -201,9 +207,10 @@ def _cuda(t, name):
 
 
 def _same_device(ref, *named):
+    device = ref.device
     for name, t in named:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _fp32_vec(t, name, C):
@@ -731,10 +738,11 @@ def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, *, residual=None, bias
 def _gn_dims(x, groups):
     if _cuda(x, "x").dim() < 2:
         raise ValueError("channels-last GroupNorm wants a contiguous [N, ..., C] tensor")
-    N, C = x.shape[0], x.shape[-1]
+    shape = x.shape
+    N, C = shape[0], shape[-1]
     if groups < 1 or C % groups:
         raise ValueError(f"{groups} groups do not divide {C} channels")
-    return N, math.prod(x.shape[1:-1]), C
+    return N, x.numel() // (N * C) if N and C else math.prod(shape[1:-1]), C
 
 
 def _gn_act(act):
@@ -764,7 +772,8 @@ def gn_nhwc_forward_train(x, groups, gamma=None, beta=None, eps=1e-5, *, act=Non
         stats = torch.empty(3, N, groups, dtype=torch.float32, device=x.device)
     else:
         _fp32_vec(stats, "stats", 3 * N * groups)
-    ws = gn_nhwc_workspace(x, groups) if ws is None else _cuda(ws, "ws")
+    if ws is None:
+        ws = _workspace("gbn_gn_nhwc_workspace_bytes", x.device, N, S, C, groups)
     _same_device(x, ("y", y), ("stats", stats), ("ws", ws), ("gamma", gamma), ("beta", beta))
     _call(x.device, "gbn_gn_nhwc_forward_train", _ptr(x), _code(x.dtype), N, S, C, groups,
           _ptr(gamma), _ptr(beta), float(eps), code, float(slope), _ptr(y), _ptr(stats),
@@ -791,7 +800,8 @@ def gn_nhwc_backward(x, dy, stats, gamma=None, beta=None, *, act=None, slope=0.0
         dbeta = torch.empty(C, dtype=torch.float32, device=x.device)
     for name, t in (("gamma", gamma), ("beta", beta), ("dgamma", dgamma), ("dbeta", dbeta)):
         _fp32_vec(t, name, C)
-    ws = gn_nhwc_workspace(x, groups) if ws is None else _cuda(ws, "ws")
+    if ws is None:
+        ws = _workspace("gbn_gn_nhwc_workspace_bytes", x.device, N, S, C, groups)
     _same_device(x, ("dy", dy), ("stats", stats), ("gamma", gamma), ("beta", beta), ("dx", dx),
                  ("dgamma", dgamma), ("dbeta", dbeta), ("ws", ws))
     _call(x.device, "gbn_gn_nhwc_backward", _ptr(x), _ptr(dy), _code(x.dtype), N, S, C, groups,
