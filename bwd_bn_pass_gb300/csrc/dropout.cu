@@ -89,10 +89,10 @@ template <typename T> struct ColSum {
 
 // A block is 2^ltx chunks x 256 / 2^ltx rows.
 template <typename T, bool BWD, bool RES>
-__global__ void __launch_bounds__(kDThreads, 4)
+__global__ void __launch_bounds__(kDThreads, kDBlocksPerSm)
     dropout_rows_kernel(const DropArgs a) {
   constexpr bool COMP = sizeof(T) == 4;
-  constexpr int U = RES ? 1 : 2;  // rows in flight (per thread; 32 bytes or more)
+  constexpr int U = 2;  // rows in flight (four: 85 against 71 us for [8192, 8192] bf16)
   using C8 = Chunk8<T>;
   __shared__ DF red[BWD ? kDThreads / 32 : 1][BWD ? 32 * 8 : 1];  // [warp][column of the tile]
   const int TX = 1 << a.ltx, TY = kDThreads >> a.ltx;

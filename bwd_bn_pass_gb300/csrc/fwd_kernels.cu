@@ -364,39 +364,47 @@ __global__ void __launch_bounds__(kThreads, 4) row_fwd_warp_kernel(FwdArgs a) {
   }
 }
 
+// Blocks of four warps per SM of the kernel below (its registers grow with KV).
+template <int KV> constexpr int kRngBlocks = KV > 4 ? 3 : KV > 2 ? 4 : 6;
+
 // The drawn mask, rows of at most 256 vectors: one warp per row, the row in
 // registers as packed fp32 pairs (KV vectors a lane: lane, lane + 32, ...).
-// All loads of a row are issued first; z goes out as soon as it is formed, and
-// the registers then hold z - shift for both statistics passes and y.  Bound:
-// instruction issue (the generator is a quarter of ~25 an element), then DRAM.
+// The loads of a warp's next row are issued as soon as this one's z is formed,
+// and wait under its statistics and outputs; z goes out at once, and the
+// registers then hold z - shift for both statistics passes and y.  Bound:
+// instruction issue (the generator is a quarter of ~30 an element), then DRAM.
 template <typename T, int KV>
-__global__ void __launch_bounds__(128, KV > 4 ? 4 : 6) row_fwd_rng_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const FwdArgs a) {
   constexpr int VE = 16 / sizeof(T);
   constexpr int NP = VE / 2;
   using V = Vec<T, VE>;
   const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  const bool tail = lane + 32 * (KV - 1) < a.Hv;  // the last vector is this lane's too
+  typename V::raw rx[KV], rr[KV];
+  auto load = [&](int64_t r) {
+    const T* x = static_cast<const T*>(a.x) + r * a.H + lane * VE;
+    const T* res = static_cast<const T*>(a.res) + r * a.H + lane * VE;
+#pragma unroll
+    for (int k = 0; k < KV; ++k)
+      if (k < KV - 1 || tail) {
+        rx[k] = V::ld(x + k * 32 * VE);
+        rr[k] = V::ld(res + k * 32 * VE);
+      }
+  };
+#pragma unroll
+  for (int k = 0; k < KV; ++k) rx[k] = rr[k] = typename V::raw{};
+  const int64_t nteams = (int64_t)gridDim.x * 4;
+  int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r < a.R) load(r);
   philox_fill(keys, a.rng);
   __syncthreads();
-  if (r >= a.R) return;
-  const int64_t ro = r * (int64_t)a.H + lane * VE;
-  const bool tail = lane + 32 * (KV - 1) < a.Hv;  // the last vector is this lane's too
-  const T* x = static_cast<const T*>(a.x) + ro;
-  const T* res = static_cast<const T*>(a.res) + ro;
-  typename V::raw rx[KV], rr[KV];
-#pragma unroll
-  for (int k = 0; k < KV; ++k) {
-    rx[k] = rr[k] = typename V::raw{};
-    if (k < KV - 1 || tail) {
-      rx[k] = V::ld(x + k * 32 * VE);
-      rr[k] = V::ld(res + k * 32 * VE);
-    }
-  }
   Philox<true> gen;
   gen.load(a.rng, keys);
   const T* bias = static_cast<const T*>(a.bias) + lane * VE;
   const f2 scale2 = f2_splat(a.scale);
+  for (; r < a.R; r += nteams) {
+  const int64_t ro = r * (int64_t)a.H + lane * VE;
   f2 z[KV][NP];
 #pragma unroll
   for (int k = 0; k < KV; ++k) {
@@ -419,6 +427,7 @@ __global__ void __launch_bounds__(128, KV > 4 ? 4 : 6) row_fwd_rng_kernel(const 
     if (a.z != nullptr && (k < KV - 1 || tail))
       store_pairs<T, VE>(static_cast<T*>(a.z) + ro + k * 32 * VE, z[k]);
   }
+  if (r + nteams < a.R) load(r + nteams);
   const float shift = __shfl_sync(0xffffffffu, f2_unpack(z[0][0]).x, 0);
   const f2 nshift2 = f2_splat(-shift);
   f2 s = 0ull;
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(128, KV > 4 ? 4 : 6) row_fwd_rng_kernel(const 
   const f2 rs2 = f2_splat(rs);
 #pragma unroll
   for (int k = 0; k < KV; ++k) {
-    if (k == KV - 1 && !tail) break;
+    if (k == KV - 1 && !tail) continue;
     const int64_t j = (int64_t)(lane + 32 * k) * VE;
     f2 o[NP];
 #pragma unroll
@@ -467,6 +476,7 @@ __global__ void __launch_bounds__(128, KV > 4 ? 4 : 6) row_fwd_rng_kernel(const 
   if (lane == 0) {
     a.mean[r] = shift + md;
     a.rstd[r] = rs;
+  }
   }
 }
 
@@ -537,10 +547,11 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
 
 // Row kernels of at most 256 vectors with the drawn mask: KV = vectors a lane.
 template <typename T, int KV>
-cudaError_t launch_rng(const FwdArgs& a, cudaStream_t st) {
+cudaError_t launch_rng(const FwdArgs& a, const DevInfo& dev, cudaStream_t st) {
   if constexpr (KV > 1)
-    if (a.Hv <= 32 * (KV - 1)) return launch_rng<T, KV - 1>(a, st);
-  const dim3 grid((unsigned)((a.R + 3) / 4)), block(128);
+    if (a.Hv <= 32 * (KV - 1)) return launch_rng<T, KV - 1>(a, dev, st);
+  const int64_t blocks = (a.R + 3) / 4, cap = (int64_t)dev.sms * kRngBlocks<KV>;
+  const dim3 grid((unsigned)(blocks < cap ? blocks : cap)), block(128);
   return launch(row_fwd_rng_kernel<T, KV>, grid, block, 0, st, false, a);
 }
 
@@ -548,7 +559,7 @@ template <typename T, int KIND>
 cudaError_t launch_kind(const FwdArgs& a, bool vec_ok, const DevInfo& dev, cudaStream_t st) {
   const int64_t R = a.R;
   if constexpr (KIND == kRowLnRng) {
-    if (vec_ok && a.Hv <= 256 && R <= ((int64_t)1 << 32)) return launch_rng<T, 8>(a, st);
+    if (vec_ok && a.Hv <= 256) return launch_rng<T, 8>(a, dev, st);
   } else if (vec_ok && a.Hv <= 256) {
     // one warp per row, 8 per block; z of each row in shared memory
     constexpr int VE = 16 / sizeof(T);

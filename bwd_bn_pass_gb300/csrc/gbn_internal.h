@@ -366,7 +366,7 @@ cudaError_t rope_launch(const RopePlan& p, const RopePtrs& q, int dir, int dtype
 
 // ------------------------------------------ dropout, mask never stored --
 
-constexpr int kDBlocksPerSm = 4;  // 256-thread blocks per SM the grid fills
+constexpr int kDBlocksPerSm = 3;  // 256-thread blocks per SM the grid fills
 
 // Generator arguments for drop probability p in [0, 1].
 RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state);
