@@ -371,7 +371,8 @@ template <int KV> constexpr int kRngBlocks = KV > 4 ? 3 : KV > 2 ? 4 : 6;
 // registers as packed fp32 pairs (KV vectors a lane: lane, lane + 32, ...).
 // The loads of a warp's next row are issued as soon as this one's z is formed,
 // and wait under its statistics and outputs; z goes out at once, and the
-// registers then hold z - shift for both statistics passes and y.  Bound:
+// registers then hold z - shift for both statistics passes and y.  Bias, gamma
+// and beta lie in shared memory (the rows streaming through L1 evict them).  Bound:
 // instruction issue (the generator is a quarter of ~30 an element), then DRAM.
 template <typename T, int KV>
 __global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const FwdArgs a) {
@@ -398,10 +399,15 @@ __global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const 
   int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (r < a.R) load(r);
   philox_fill(keys, a.rng);
+  __shared__ typename V::raw par[3][32 * KV];  // bias, gamma, beta
+  for (int v = threadIdx.x; v < a.Hv; v += blockDim.x) {
+    if (a.bias != nullptr) par[0][v] = V::ld(static_cast<const T*>(a.bias) + v * VE);
+    if (a.w != nullptr) par[1][v] = V::ld(static_cast<const T*>(a.w) + v * VE);
+    if (a.beta != nullptr) par[2][v] = V::ld(static_cast<const T*>(a.beta) + v * VE);
+  }
   __syncthreads();
   Philox<true> gen;
   gen.load(a.rng, keys);
-  const T* bias = static_cast<const T*>(a.bias) + lane * VE;
   const f2 scale2 = f2_splat(a.scale);
   for (; r < a.R; r += nteams) {
   const int64_t ro = r * (int64_t)a.H + lane * VE;
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const 
     to_pairs<T, VE>(rr[k], z[k]);
     if (a.bias != nullptr && (k < KV - 1 || tail)) {
       f2 bv[NP];
-      to_pairs<T, VE>(V::ld(bias + k * 32 * VE), bv);
+      to_pairs<T, VE>(par[0][lane + 32 * k], bv);
 #pragma unroll
       for (int p = 0; p < NP; ++p) xv[p] = f2_add(xv[p], bv[p]);
     }
@@ -455,19 +461,18 @@ __global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const 
 #pragma unroll
   for (int k = 0; k < KV; ++k) {
     if (k == KV - 1 && !tail) continue;
-    const int64_t j = (int64_t)(lane + 32 * k) * VE;
     f2 o[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) o[p] = f2_mul(f2_add(z[k][p], nmd2), rs2);
     if (a.w != nullptr) {
       f2 g[NP];
-      to_pairs<T, VE>(V::ld(static_cast<const T*>(a.w) + j), g);
+      to_pairs<T, VE>(par[1][lane + 32 * k], g);
 #pragma unroll
       for (int p = 0; p < NP; ++p) o[p] = f2_mul(o[p], g[p]);
     }
     if (a.beta != nullptr) {
       f2 b[NP];
-      to_pairs<T, VE>(V::ld(static_cast<const T*>(a.beta) + j), b);
+      to_pairs<T, VE>(par[2][lane + 32 * k], b);
 #pragma unroll
       for (int p = 0; p < NP; ++p) o[p] = f2_add(o[p], b[p]);
     }
