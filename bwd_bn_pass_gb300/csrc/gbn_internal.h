@@ -359,6 +359,7 @@ bool rope_plan(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, bool in
                int vec_max, int dir, const DevInfo& dev, RopePlan* p);
 size_t rope_ws_bound(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, int dtype,
                      const DevInfo& dev);
+cudaError_t rope_configure();  // shared-memory limits (called from device_info)
 // dir: 0 forward, 1 backward (without wq: the rotation back of dy).
 cudaError_t rope_launch(const RopePlan& p, const RopePtrs& q, int dir, int dtype, int64_t T,
                         int64_t H, int64_t HQ, int64_t D, int64_t rot, bool inter, float scale,

@@ -295,6 +295,33 @@ __global__ void __launch_bounds__(kRThreads, 4) rope_fwd_kernel(const RopeArgs a
   }
 }
 
+// 8- or 16-byte asynchronous copy into this thread's shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows of the backward in flight per team: this many stages of private shared
+// memory per thread, one being read, one just read (refilled only after its
+// values were used), the rest on their way.
+constexpr int kRopeStages = 3;
+// Full rows of 8- or 16-byte vectors go through them; a row ahead in registers
+// (the other form) left 32 KB in flight per SM: 45 against 41 us for 8192 tokens of 32 heads (six stages: 53).
+template <typename T, int VEC, bool FULL> constexpr bool kRopeAsync = FULL && sizeof(T) * VEC >= 8;
+template <typename T, int VEC, int NS, bool FULL>
+constexpr size_t rope_bwd_smem() {
+  const size_t red = sizeof(DF) * 2 * NS * VEC * kRThreads;
+  const size_t ring = kRopeAsync<T, VEC, FULL>
+                          ? (size_t)kRopeStages * kRThreads * (4 * NS * VEC * sizeof(T) + 4)
+                          : 0;
+  return red > ring ? red : ring;
+}
+
 // Backward with the norm.  blockIdx.y: a chunk of query heads (below cq) or of
 // key heads; blocks stride over the tokens.  A block's weight gradient goes to
 // its row of the partials.
@@ -303,7 +330,12 @@ __global__ void __launch_bounds__(kRThreads, 2) rope_bwd_kernel(const RopeArgs a
   constexpr bool COMP = sizeof(T) == 4;
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
-  extern __shared__ DF red[];  // [teams][2 * NS * VEC * L]
+  constexpr bool ASYNC = kRopeAsync<T, VEC, FULL>;
+  extern __shared__ __align__(16) unsigned char rope_smem[];
+  DF* red = reinterpret_cast<DF*>(rope_smem);  // [teams][2 * NS * VEC * L], after the rows
+  // [stage][vector][thread], then the rows' rstd [stage][thread]
+  auto ring = reinterpret_cast<typename V::raw(*)[4 * NS][kRThreads]>(rope_smem);
+  auto ring_rs = reinterpret_cast<float(*)[kRThreads]>(rope_smem + sizeof(ring[0]) * kRopeStages);
   const int l = threadIdx.x & (a.L - 1), team = threadIdx.x / a.L, teams = kRThreads / a.L;
   const RopeChunk ch = rope_chunk(a, blockIdx.y);
   const T* w = static_cast<const T*>(ch.is_q ? a.wq : a.wk);
@@ -323,6 +355,33 @@ __global__ void __launch_bounds__(kRThreads, 2) rope_bwd_kernel(const RopeArgs a
   }
   const float inv_D = 1.f / (float)a.D;
   const int nh = ch.h1 - ch.h0;
+  // ASYNC: the next row to copy (token block, head) and its stage
+  int64_t ptb = (int64_t)blockIdx.x * teams;
+  int phd = 0, pst = 0, st = 0;
+  auto post = [&] {
+    if (ptb < a.T) {
+      const int64_t tt = min(ptb + team, a.T - 1);
+      const T* p = static_cast<const T*>(a.x) + tt * a.xt + (int64_t)(ch.h0 + phd) * a.xh;
+      const T* q = static_cast<const T*>(a.dy) + tt * a.dt + (int64_t)(ch.h0 + phd) * a.dh;
+      constexpr int B = sizeof(T) * VEC;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        copy_async<B>(&ring[pst][4 * s][threadIdx.x], p + sl.ia[s]);
+        copy_async<B>(&ring[pst][4 * s + 1][threadIdx.x], p + sl.ib[s]);
+        copy_async<B>(&ring[pst][4 * s + 2][threadIdx.x], q + sl.ia[s]);
+        copy_async<B>(&ring[pst][4 * s + 3][threadIdx.x], q + sl.ib[s]);
+      }
+      copy_async<4>(&ring_rs[pst][threadIdx.x], a.rstd + tt * a.H + ch.h0 + phd);
+      if (++phd == nh) {
+        phd = 0;
+        ptb += (int64_t)gridDim.x * teams;
+      }
+    }
+    pst = pst + 1 == kRopeStages ? 0 : pst + 1;
+    copy_commit();  // empty where there is no row: the count of groups stays in step
+  };
+  if constexpr (ASYNC)
+    for (int k = 0; k < kRopeStages - 1; ++k) post();
   for (int64_t tb = (int64_t)blockIdx.x * teams; tb < a.T; tb += (int64_t)gridDim.x * teams) {
     const int64_t t = tb + team;
     const bool live = t < a.T;
@@ -334,6 +393,19 @@ __global__ void __launch_bounds__(kRThreads, 2) rope_bwd_kernel(const RopeArgs a
     typename V::raw xa[NS], xb[NS], da[NS], db[NS];
     float rs = 0.f;
     auto load = [&](int h) {
+      if constexpr (ASYNC) {
+        copy_wait<kRopeStages - 1>();
+        rs = live ? ring_rs[st][threadIdx.x] : 0.f;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          xa[s] = ring[st][4 * s][threadIdx.x];
+          xb[s] = ring[st][4 * s + 1][threadIdx.x];
+          da[s] = ring[st][4 * s + 2][threadIdx.x];
+          db[s] = ring[st][4 * s + 3][threadIdx.x];
+        }
+        st = st + 1 == kRopeStages ? 0 : st + 1;
+        return;
+      }
       rs = live ? rp[h] : 0.f;  // 0: an idle team adds nothing
       const T* p = x + (int64_t)h * a.xh;
       const T* q = d + (int64_t)h * a.dh;
@@ -345,9 +417,13 @@ __global__ void __launch_bounds__(kRThreads, 2) rope_bwd_kernel(const RopeArgs a
         ld_vec<T, VEC, FULL>(q + sl.ib[s], sl.vb[s], db[s]);
       }
     };
-    load(0);  // on their way while the sines and cosines are formed
+    if (!ASYNC) load(0);  // on their way while the sines and cosines are formed
     sl.template angles<true, !COMP>(a, l, rope_pos(a, tt));
     for (int h = 0; h < nh; ++h) {
+      if constexpr (ASYNC) {
+        post();  // into the stage read in the round before
+        load(h);
+      }
       f2 g0[NS][NP], g1[NS][NP], x0[NS][NP], x1[NS][NP];
       const float r = rs;
       const f2 r2 = f2_splat(r);
@@ -358,7 +434,7 @@ __global__ void __launch_bounds__(kRThreads, 2) rope_bwd_kernel(const RopeArgs a
         to_pairs<T, VEC>(da[s], g0[s]);
         to_pairs<T, VEC>(db[s], g1[s]);
       }
-      if (h + 1 < nh) load(h + 1);
+      if (!ASYNC && h + 1 < nh) load(h + 1);
       f2 q = 0ull;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
@@ -394,6 +470,10 @@ __global__ void __launch_bounds__(kRThreads, 2) rope_bwd_kernel(const RopeArgs a
     }
   }
   // the block's teams, added in order
+  if constexpr (ASYNC) {
+    copy_wait<0>();
+    __syncthreads();  // every thread has read its rows: the memory is reused
+  }
   const int per = 2 * NS * VEC;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
@@ -474,9 +554,18 @@ cudaError_t rope_run(const RopePlan& p, const RopeArgs& a, int dir, cudaStream_t
     return launch(rope_fwd_kernel<T, VEC, NS, INTER, false, true, FULL>, grid, block, 0, st, false,
                   a);
   }
-  const size_t smem = sizeof(DF) * 2 * NS * VEC * kRThreads;
   return launch(rope_bwd_kernel<T, VEC, NS, INTER, FULL>,
-                dim3((unsigned)p.bx, (unsigned)(a.cq + a.ck)), block, smem, st, false, a);
+                dim3((unsigned)p.bx, (unsigned)(a.cq + a.ck)), block,
+                rope_bwd_smem<T, VEC, NS, FULL>(), st, false, a);
+}
+template <typename T, int VEC, int NS>
+cudaError_t rope_configure_one() {
+  constexpr size_t bytes = rope_bwd_smem<T, VEC, NS, true>();
+  const cudaError_t e = cudaFuncSetAttribute(rope_bwd_kernel<T, VEC, NS, false, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(rope_bwd_kernel<T, VEC, NS, true, true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 template <typename T, int VEC, int NS>
 cudaError_t rope_run_layout(const RopePlan& p, const RopeArgs& a, int dir, bool inter,
@@ -509,6 +598,14 @@ cudaError_t rope_dispatch(const RopePlan& p, const RopeArgs& a, int dir, bool in
 }
 
 }  // namespace
+
+cudaError_t rope_configure() {
+  for (cudaError_t e : {rope_configure_one<bf16, 8, 1>(), rope_configure_one<bf16, 4, 1>(),
+                        rope_configure_one<bf16, 4, 2>(), rope_configure_one<float, 4, 1>(),
+                        rope_configure_one<float, 4, 2>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
 
 // `vec_max`: the widest vector that alignment and strides allow.
 bool rope_plan(int64_t T, int64_t H, int64_t HQ, int64_t D, int64_t rot, bool inter, int dtype,
