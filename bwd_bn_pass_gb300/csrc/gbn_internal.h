@@ -306,6 +306,7 @@ cudaError_t selftest_bounded_wait(int* status, uint64_t limit_ns, cudaStream_t s
 struct GnPlan {
   int64_t N = 0, S = 0, C = 0, G = 0;  // samples, rows per sample, channels, groups
   bool backward = false;
+  bool small = false;       // one launch, a cluster of `slices` blocks per sample
   int vec = 1;              // channels per vector (divides C)
   int TX = 1, TY = 1;       // block shape: vectors x rows
   int tiles = 1;            // channel tiles of TX vectors

@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kGThreads = 256;
 constexpr int kGnTogether = 2; // groups whose reductions overlap
+constexpr int kGnSmallRows = 16;
 constexpr int kGnFewRows = 8;  // thread rows that one thread adds up per channel
 
 struct GnGeom {
@@ -168,16 +169,16 @@ __device__ __forceinline__ f2 gn_gated(f2 d, f2 npre, float slope) {
 
 // ---------------------------------------------------------- statistics --
 
+template <int VEC> constexpr int kGnStatsSmem = kGThreads * VEC * 12;
+
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kGThreads, 3) gn_stats_kernel(const GnArgs a) {
+__device__ __forceinline__ void gn_stats(const GnArgs& a, const GnBlock& b, unsigned char* smem) {
   constexpr int U = 4;  // rows of a chunk
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
-  __shared__ float2 acc[kGThreads * VEC];  // [ty][channel of the tile]: mean - K, M2
-  __shared__ float Ks[kGThreads * VEC];    // shifts: x[n, 0, c]
-  pdl_launch_dependents();
+  float2* acc = reinterpret_cast<float2*>(smem);  // [ty][channel of the tile]: mean - K, M2
+  float* Ks = reinterpret_cast<float*>(smem + kGThreads * VEC * 8);  // shifts: x[n, 0, c]
   const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g, blockIdx.x);
   const T* xs = static_cast<const T*>(a.x) + (int64_t)b.n * g.S * g.C;
   const int W = g.TX * VEC;  // channels of a full tile
   if (b.active) {
@@ -362,6 +363,13 @@ __global__ void __launch_bounds__(kGThreads, 3) gn_stats_kernel(const GnArgs a) 
   }
 }
 
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kGThreads, 3) gn_stats_kernel(const GnArgs a) {
+  __shared__ __align__(16) unsigned char smem[kGnStatsSmem<VEC>];
+  pdl_launch_dependents();
+  gn_stats<T, VEC>(a, gn_block<VEC>(a.g, blockIdx.x), smem);
+}
+
 // Tiles that hold channels of group gi: first and one past the last.
 template <int VEC>
 __device__ __forceinline__ void gn_tiles_of(const GnGeom& g, int gi, int& t0, int& t1) {
@@ -462,16 +470,19 @@ __device__ __forceinline__ void gn_const(const float* arr, int tx, f2 (&p)[kPair
 // end: what the first pass read last is likeliest in L2.
 __device__ __forceinline__ uint32_t gn_from_last() { return gridDim.x - 1 - blockIdx.x; }
 
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_apply_kernel(const GnArgs a) {
+template <int VEC> constexpr int kGnApplySmem = kGThreads * VEC * 12 + kGThreads * 8;
+
+// `ready` returns once the statistics pass is complete; fin: per group of the
+// tile mean hi, lo, rstd.
+template <typename T, int VEC, int ACT, typename Ready>
+__device__ __forceinline__ void gn_apply(const GnArgs& a, const GnBlock& b, unsigned char* smem,
+                                         float3* fin, Ready ready) {
   constexpr int U = 4;
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
-  extern __shared__ float3 fin[];  // per group of the tile: mean hi, lo, rstd
-  __shared__ __align__(16) float cst[3][kGThreads * VEC];  // mean hi, -scale, -shift
-  __shared__ float red[2 * kGThreads];
+  auto cst = reinterpret_cast<float(*)[kGThreads * VEC]>(smem);  // mean hi, -scale, -shift
+  float* red = reinterpret_cast<float*>(smem + kGThreads * VEC * 12);
   const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g, gn_from_last());
   const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
   const T* xs = static_cast<const T*>(a.x) + base;
   T* ys = static_cast<T*>(a.out) + base;
@@ -491,7 +502,7 @@ __global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_apply_kernel(co
     }
   };
   load();
-  pdl_wait();
+  ready();
   // Sums relative to the middle slice's mean m0, which is one of the summands:
   // sum n (m - m0)^2 exceeds the spread between the slices at most slices-fold,
   // so the final difference is safe.
@@ -550,6 +561,32 @@ __global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_apply_kernel(co
     if (u < left) row(u);
 }
 
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_apply_kernel(const GnArgs a) {
+  extern __shared__ float3 fin[];
+  __shared__ __align__(16) unsigned char smem[kGnApplySmem<VEC>];
+  gn_apply<T, VEC, ACT>(a, gn_block<VEC>(a.g, gn_from_last()), smem, fin, pdl_wait);
+}
+
+// Release and acquire among the blocks of a cluster (global memory too), and a
+// block barrier.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Both passes in one launch, a cluster of `slices` blocks per sample: the
+// group partials go through L2 and the cluster barrier.
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGThreads, VEC > 4 ? 3 : 4) gn_small_forward_kernel(const GnArgs a) {
+  extern __shared__ float3 fin[];
+  __shared__ __align__(16) unsigned char
+      smem[kGnApplySmem<VEC> > kGnStatsSmem<VEC> ? kGnApplySmem<VEC> : kGnStatsSmem<VEC>];
+  const GnBlock b = gn_block<VEC>(a.g, blockIdx.x);
+  gn_stats<T, VEC>(a, b, smem);
+  gn_apply<T, VEC, ACT>(a, b, smem, fin, cluster_sync);
+}
+
 // -------------------------------------------------------- backward sums --
 
 // Running sum of pairs: fp32 storage carries the errors (its weight gradients
@@ -564,18 +601,16 @@ template <typename T> struct GnSum {
 
 // Per channel of the tile: sum e and sum e*xhat of the block's rows, to the
 // column partials; and per group the sums of gamma*e and gamma*e*xhat.
+template <int VEC> constexpr int kGnSumsSmem = kGThreads * VEC * 16;
+
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
-    gn_sums_kernel(const GnArgs a) {
+__device__ __forceinline__ void gn_sums(const GnArgs& a, const GnBlock& b, unsigned char* smem) {
   constexpr int U = 4;  // rows in flight (two inputs)
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
-  __shared__ __align__(16) DF sab[2][kGThreads * VEC];  // [ty][channel]
-  DF* sa = sab[0];
-  DF* sb = sab[1];
-  pdl_launch_dependents();
+  DF* sa = reinterpret_cast<DF*>(smem);  // [ty][channel]
+  DF* sb = sa + kGThreads * VEC;
   const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g, blockIdx.x);
   const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
   const T* xs = static_cast<const T*>(a.x) + base;
   const T* ds = static_cast<const T*>(a.dy) + base;
@@ -710,6 +745,14 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
   }
 }
 
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
+    gn_sums_kernel(const GnArgs a) {
+  __shared__ __align__(16) unsigned char smem[kGnSumsSmem<VEC>];
+  pdl_launch_dependents();
+  gn_sums<T, VEC, ACT>(a, gn_block<VEC>(a.g, blockIdx.x), smem);
+}
+
 // ------------------------------------------------------- weight gradients --
 
 // dgamma and dbeta: the channel partials of every sample and slice, added in a
@@ -774,17 +817,18 @@ __global__ void __cluster_dims__(kGnWCluster, 1, 1) __launch_bounds__(1024)
 
 // ------------------------------------------------------------------- dx --
 
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
-    gn_dx_kernel(const GnArgs a) {
+template <int VEC> constexpr int kGnDxSmem = kGThreads * VEC * 24 + kGThreads * 8;
+
+// kk: k0, k1 of the tile's groups.
+template <typename T, int VEC, int ACT, typename Ready>
+__device__ __forceinline__ void gn_dx(const GnArgs& a, const GnBlock& b, unsigned char* smem,
+                                      float2* kk, Ready ready) {
   constexpr int U = 4;
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
-  extern __shared__ float2 kk[];  // k0, k1 of the tile's groups
-  __shared__ __align__(16) float cst[6][kGThreads * VEC];  // per channel
-  __shared__ float red[2 * kGThreads];
+  auto cst = reinterpret_cast<float(*)[kGThreads * VEC]>(smem);  // per channel
+  float* red = reinterpret_cast<float*>(smem + kGThreads * VEC * 24);
   const GnGeom& g = a.g;
-  const GnBlock b = gn_block<VEC>(g, gn_from_last());
   const int64_t base = ((int64_t)b.n * g.S + b.r0) * g.C;
   const T* xs = static_cast<const T*>(a.x) + base;
   const T* ds = static_cast<const T*>(a.dy) + base;
@@ -811,8 +855,7 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
     }
   };
   load();
-  pdl_wait();
-  pdl_launch_dependents();
+  ready();
   gn_walk<VEC, 2>(
       a, b, red, [](const float2*) {},
       [](float(&acc)[2], float2 v, float, float) {
@@ -869,7 +912,49 @@ __global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
     if (u < left) row(u);
 }
 
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
+    gn_dx_kernel(const GnArgs a) {
+  extern __shared__ float2 kk[];
+  __shared__ __align__(16) unsigned char smem[kGnDxSmem<VEC>];
+  gn_dx<T, VEC, ACT>(a, gn_block<VEC>(a.g, gn_from_last()), smem, kk, [] {
+    pdl_wait();
+    pdl_launch_dependents();
+  });
+}
+
+// As gn_small_forward_kernel; the weight gradients' launch follows.
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGThreads, sizeof(T) * VEC > 8 ? 3 : 4)
+    gn_small_backward_kernel(const GnArgs a) {
+  extern __shared__ float2 kk[];
+  __shared__ __align__(16) unsigned char smem[kGnDxSmem<VEC>];
+  static_assert(kGnDxSmem<VEC> >= kGnSumsSmem<VEC>, "one buffer for both passes");
+  pdl_launch_dependents();
+  const GnBlock b = gn_block<VEC>(a.g, blockIdx.x);
+  gn_sums<T, VEC, ACT>(a, b, smem);
+  gn_dx<T, VEC, ACT>(a, b, smem, kk, cluster_sync);
+}
+
 // ----------------------------------------------------------------- host --
+
+// One launch whose clusters are a sample's slices.
+cudaError_t gn_launch_cluster(void (*kern)(GnArgs), const GnPlan& p, size_t smem, const GnArgs& a,
+                              cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.N, (unsigned)p.slices);
+  cfg.blockDim = dim3((unsigned)p.threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = (unsigned)p.slices;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
 
 // Both passes of a direction.
 template <typename T, int VEC, int ACT>
@@ -877,6 +962,14 @@ cudaError_t gn_run(const GnPlan& p, const GnArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)(p.N * p.tiles), (unsigned)p.slices);
   const dim3 block((unsigned)p.threads);
   const size_t groups = (size_t)p.tile_groups;
+  if (p.small) {
+    if (!p.backward)
+      return gn_launch_cluster(gn_small_forward_kernel<T, VEC, ACT>, p, groups * sizeof(float3), a,
+                               st);
+    if constexpr (VEC <= 4)
+      return gn_launch_cluster(gn_small_backward_kernel<T, VEC, ACT>, p, groups * sizeof(float2), a,
+                               st);
+  }
   if (!p.backward) {
     const cudaError_t e = launch(gn_stats_kernel<T, VEC>, grid, block, 0, st, false, a);
     if (e != cudaSuccess) return e;
@@ -971,6 +1064,11 @@ bool gn_plan(int64_t N, int64_t S, int64_t C, int64_t G, int vec, int64_t esize,
   const int64_t rounds = (S + round - 1) / round;
   int64_t s = per < rounds ? per : rounds;
   if (s < 1) s = 1;
+  // one launch, a cluster of at most eight blocks per sample, while a thread's
+  // share stays below kGnSmallRows rows
+  const int64_t few = (S + (int64_t)p->TY * kGnSmallRows - 1) / ((int64_t)p->TY * kGnSmallRows);
+  p->small = p->tiles == 1 && few <= 8;
+  if (p->small) s = rounds < 8 ? rounds : 8;
   // 32-bit offsets inside a slice
   const int64_t least = (S * C * esize + ((int64_t)1 << 31) - 1) >> 31;
   if (s < least) s = least;
