@@ -288,7 +288,7 @@ def test_offsets_past_32_bits(gbn, dev):
 
 
 LN_SHAPES = [(1, 8), (3, 16), (7, 1001), (70, 256), (33, 1600), (5, 20000), (12, 1008), (2, 4),
-             (4, 1), (9, 4096), (40, 72)]
+             (4, 1), (9, 4096), (40, 72), (2600, 512), (8, 1024), (1300, 520), (3, 2048)]
 
 
 @pytest.mark.gpu
@@ -322,7 +322,8 @@ def test_layernorm(gbn, dev, R, H, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("R,H,mis", [(40, 512, False), (9, 77, False), (6, 64, True)])
+@pytest.mark.parametrize("R,H,mis", [(40, 512, False), (9, 77, False), (6, 64, True),
+                                     (2500, 1024, False)])
 def test_layernorm_variants(gbn, dev, R, H, mis):
     """No bias, saved z, fp32 residual gradient, an extra gradient at z, no
     affine, misaligned input; two runs give the same bits; the drawn mask
