@@ -26,7 +26,12 @@
 // sum (d - mean_d)^2 (never E[z^2] - mean^2), and y from (d - mean_d), so a
 // row whose mean is large next to its spread loses nothing to the rounding
 // of the mean (the same shifted form as the BatchNorm kernels).  Reductions
-// are fixed trees, so results are bit-deterministic.
+// are fixed trees, so results are bit-deterministic.  The rows with the drawn
+// mask (below) need no shift: they take the plain mean m, and the second pass
+// also sums c = z - m, whose mean is what m's rounding missed (mean = m +
+// mean(c), var = mean(c^2) - mean(c)^2).  For rows around zero the saved mean
+// is ten times closer than the shifted form's, which rounds at the size of
+// the first element, and a first element far from the others costs nothing.
 //
 // The fused form also runs with the counter-based mask of philox.cuh
 // (kRowLnRng), a dropped element contributing exactly 0 whatever it holds:
@@ -82,6 +87,19 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
     return s;
   }
 }
+
+// The drawn rows' second pass: the sums of c and c^2 over H elements, c = z -
+// m, give what the mean m lacks, and the variance.  A row that is not finite
+// keeps m as its mean (an infinity, as its plain sum gives).
+struct Centred {
+  float lack, mean, rstd;
+  __device__ __forceinline__ Centred(float m, float sc, float sq, float invH, float eps) {
+    lack = sc * invH;
+    mean = isfinite(lack) ? m + lack : m;
+    const float v = fmaf(-lack, lack, sq * invH);
+    rstd = 1.f / sqrtf((v < 0.f ? 0.f : v) + eps);
+  }
+};
 
 // Mask bytes of one vector of VE elements (8 or 4 bytes).
 template <int VE>
@@ -156,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
 #pragma unroll
             for (int e = 0; e < VE; ++e)
               z[k][e] = fmaf(f[e] ? z[k][e] + bv[e] : 0.f, a.scale, rv[e]);
+            if (a.z != nullptr) V::store(static_cast<T*>(a.z) + ro + (int64_t)vi * VE, z[k]);
           } else {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
@@ -173,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
     // block team it goes through red[31] (team_sum uses red[0..7]); the
     // previous row's reads of red[31] precede that row's later barriers.
     float shift = 0.f;
-    if constexpr (KIND != GBN_ROW_RMS) {
+    if constexpr (KIND != GBN_ROW_RMS && !RNG) {
       if constexpr (WARP) {
         shift = __shfl_sync(0xffffffffu, z[0][0], 0);
       } else {
@@ -190,12 +209,12 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
         for (int e = 0; e < VE; ++e)
           s += KIND == GBN_ROW_RMS ? z[k][e] * z[k][e] : z[k][e] - shift;
       }
-    float md = 0.f, rs;
+    float md = 0.f, mean = 0.f, rs;
     if constexpr (KIND == GBN_ROW_RMS) {
       rs = 1.f / sqrtf(team_sum<WARP>(s, red) * invH + a.eps);
     } else {
       md = team_sum<WARP>(s, red) * invH;
-      float s2 = 0.f;
+      float s2 = 0.f, sc = 0.f;
 #pragma unroll
       for (int k = 0; k < KV; ++k)
         if (tt + k * TS < a.Hv) {
@@ -203,9 +222,20 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
           for (int e = 0; e < VE; ++e) {
             const float c = (z[k][e] - shift) - md;
             s2 = fmaf(c, c, s2);
+            if constexpr (RNG) {
+              sc += c;
+              z[k][e] = c;
+            }
           }
         }
-      rs = 1.f / sqrtf(team_sum<WARP>(s2, red) * invH + a.eps);
+      if constexpr (RNG) {
+        const float tc = team_sum<WARP>(sc, red), tq = team_sum<WARP>(s2, red);
+        const Centred f(md, tc, tq, invH, a.eps);
+        mean = f.mean, rs = f.rstd, md = f.lack;
+      } else {
+        rs = 1.f / sqrtf(team_sum<WARP>(s2, red) * invH + a.eps);
+        mean = shift + md;
+      }
     }
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
@@ -229,10 +259,11 @@ __global__ void __launch_bounds__(kThreads) row_fwd_kernel(FwdArgs a) {
         o[e] = KIND == GBN_ROW_RMS ? (z[k][e] * rs) * g[e]
                                    : fmaf(((z[k][e] - shift) - md) * rs, g[e], b[e]);
       V::store(static_cast<T*>(a.y) + ro + (int64_t)vi * VE, o);
-      if (FUSED && a.z != nullptr) V::store(static_cast<T*>(a.z) + ro + (int64_t)vi * VE, z[k]);
+      if (FUSED && !RNG && a.z != nullptr)
+        V::store(static_cast<T*>(a.z) + ro + (int64_t)vi * VE, z[k]);
     }
     if (tt == 0) {
-      if (KIND != GBN_ROW_RMS) a.mean[r] = shift + md;
+      if (KIND != GBN_ROW_RMS) a.mean[r] = mean;
       a.rstd[r] = rs;
     }
   }
@@ -371,7 +402,7 @@ template <int KV> constexpr int kRngBlocks = KV > 4 ? 3 : KV > 2 ? 4 : 6;
 // registers as packed fp32 pairs (KV vectors a lane: lane, lane + 32, ...).
 // The loads of a warp's next row are issued as soon as this one's z is formed,
 // and wait under its statistics and outputs; z goes out at once, and the
-// registers then hold z - shift for both statistics passes and y.  Bias, gamma
+// registers hold z, then z - m for the second statistics pass and y.  Bias, gamma
 // and beta lie in shared memory (the rows streaming through L1 evict them).  Bound:
 // instruction issue (the generator is a quarter of ~30 an element), then DRAM.
 template <typename T, int KV>
@@ -434,36 +465,35 @@ __global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const 
       store_pairs<T, VE>(static_cast<T*>(a.z) + ro + k * 32 * VE, z[k]);
   }
   if (r + nteams < a.R) load(r + nteams);
-  const float shift = __shfl_sync(0xffffffffu, f2_unpack(z[0][0]).x, 0);
-  const f2 nshift2 = f2_splat(-shift);
   f2 s = 0ull;
 #pragma unroll
   for (int k = 0; k < KV; ++k)
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      z[k][p] = f2_add(z[k][p], nshift2);
-      if (k == KV - 1 && !tail) z[k][p] = 0ull;
-      s = f2_add(s, z[k][p]);
-    }
+    for (int p = 0; p < NP; ++p)
+      if (k < KV - 1 || tail) s = f2_add(s, z[k][p]);
   const float invH = 1.f / (float)a.H;
-  const float md = warp_sum(f2_hsum(s)) * invH;
-  const f2 nmd2 = f2_splat(-md);
-  f2 q = 0ull;
+  const float m = warp_sum(f2_hsum(s)) * invH;
+  const f2 nm2 = f2_splat(-m);
+  f2 q = 0ull, sc = 0ull;
 #pragma unroll
   for (int k = 0; k < KV; ++k)
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      const f2 c = f2_add(z[k][p], nmd2);
-      if (k < KV - 1 || tail) q = f2_fma(c, c, q);
+      z[k][p] = f2_add(z[k][p], nm2);
+      if (k < KV - 1 || tail) {
+        sc = f2_add(sc, z[k][p]);
+        q = f2_fma(z[k][p], z[k][p], q);
+      }
     }
-  const float rs = 1.f / sqrtf(warp_sum(f2_hsum(q)) * invH + a.eps);
-  const f2 rs2 = f2_splat(rs);
+  const float tc = warp_sum(f2_hsum(sc)), tq = warp_sum(f2_hsum(q));
+  const Centred f(m, tc, tq, invH, a.eps);
+  const f2 rs2 = f2_splat(f.rstd), nlr2 = f2_splat(-f.lack * f.rstd);
 #pragma unroll
   for (int k = 0; k < KV; ++k) {
     if (k == KV - 1 && !tail) continue;
     f2 o[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) o[p] = f2_mul(f2_add(z[k][p], nmd2), rs2);
+    for (int p = 0; p < NP; ++p) o[p] = f2_fma(z[k][p], rs2, nlr2);
     if (a.w != nullptr) {
       f2 g[NP];
       to_pairs<T, VE>(par[1][lane + 32 * k], g);
@@ -479,8 +509,8 @@ __global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const 
     store_pairs<T, VE>(static_cast<T*>(a.y) + ro + k * 32 * VE, o);
   }
   if (lane == 0) {
-    a.mean[r] = shift + md;
-    a.rstd[r] = rs;
+    a.mean[r] = f.mean;
+    a.rstd[r] = f.rstd;
   }
   }
 }
@@ -516,35 +546,43 @@ __global__ void __launch_bounds__(kThreads) row_fwd_generic_kernel(FwdArgs a) {
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
     const int64_t o = r * H;
     if constexpr (RNG) rowbits_fill(rb, gen, (uint64_t)o, H);
-    const float shift = KIND == GBN_ROW_RMS ? 0.f : zval(o, 0);
+    const float shift = KIND == GBN_ROW_RMS || RNG ? 0.f : zval(o, 0);
     float s = 0.f;
     for (int64_t j = threadIdx.x; j < H; j += blockDim.x) {
       const float v = zval(o, j);
       s += KIND == GBN_ROW_RMS ? v * v : v - shift;
     }
-    float md = 0.f, rs;
+    float md = 0.f, lack = 0.f, mean = 0.f, rs;
     if constexpr (KIND == GBN_ROW_RMS) {
       rs = 1.f / sqrtf(team_sum<false>(s, red) * invH + a.eps);
     } else {
       md = team_sum<false>(s, red) * invH;
-      float s2 = 0.f;
+      float s2 = 0.f, sc = 0.f;
       for (int64_t j = threadIdx.x; j < H; j += blockDim.x) {
         const float c = (zval(o, j) - shift) - md;
         s2 = fmaf(c, c, s2);
+        if constexpr (RNG) sc += c;
       }
-      rs = 1.f / sqrtf(team_sum<false>(s2, red) * invH + a.eps);
+      if constexpr (RNG) {
+        const float tc = team_sum<false>(sc, red), tq = team_sum<false>(s2, red);
+        const Centred f(md, tc, tq, invH, a.eps);
+        mean = f.mean, rs = f.rstd, lack = f.lack;
+      } else {
+        rs = 1.f / sqrtf(team_sum<false>(s2, red) * invH + a.eps);
+        mean = shift + md;
+      }
     }
     for (int64_t j = threadIdx.x; j < H; j += blockDim.x) {
       const float v = zval(o, j);
       const float g = w ? to_f32(w[j]) : 1.f;
       const float b = (KIND != GBN_ROW_RMS && beta) ? to_f32(beta[j]) : 0.f;
-      const float out =
-          KIND == GBN_ROW_RMS ? (v * rs) * g : fmaf(((v - shift) - md) * rs, g, b);
+      const float c = RNG ? (v - md) - lack : (v - shift) - md;
+      const float out = KIND == GBN_ROW_RMS ? (v * rs) * g : fmaf(c * rs, g, b);
       static_cast<T*>(a.y)[o + j] = from_f32<T>(out);
       if (FUSED && a.z != nullptr) static_cast<T*>(a.z)[o + j] = from_f32<T>(v);
     }
     if (threadIdx.x == 0) {
-      if (KIND != GBN_ROW_RMS) a.mean[r] = shift + md;
+      if (KIND != GBN_ROW_RMS) a.mean[r] = mean;
       a.rstd[r] = rs;
     }
   }

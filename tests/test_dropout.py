@@ -372,3 +372,31 @@ def test_layernorm_long_odd_row(gbn, dev):
     ref = oracle.fused_bias_dropout_add_layer_norm_backward(
         _f64(dy), _f64(x), _f64(r), None, m, s, _f64(out["mean"]), _f64(out["rstd"]), _f64(g))
     tol.check_f32(bw["dx"], ref["dx"], "long dx")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [800, 1600, 1601, 9001])
+@pytest.mark.parametrize("kind", ["zero", "first", "offset"])
+def test_ln_dropout_mean_keeps_its_bits(gbn, H, kind):
+    """The saved mean is wrong by no more than the sums of the centred values
+    c = z - mean are: at most 48 additions in a row (a thread's own share,
+    five of a warp, eight of a block), each half a step of sum |c|, and the
+    mean's own rounding.  A first element far from the rest and a mean far
+    above the spread change nothing."""
+    g = torch.Generator().manual_seed(H)
+    z = torch.randn(5, H, generator=g)
+    if kind == "first":
+        z[:, 0] = 1e4
+    elif kind == "offset":
+        z += 1e4
+    x, res = z.cuda(), torch.zeros(5, H, device="cuda")
+    out = gbn.layernorm_dropout_forward(x, res, 0.0, (1, 2))
+    z64 = z.double()
+    mean = z64.mean(1)
+    c = (z64 - mean[:, None]).abs().mean(1)
+    bound = (48 + 1) * 2.0 ** -24 * c + 2.0 ** -24 * mean.abs()
+    assert ((out["mean"].cpu().double() - mean).abs() <= bound).all()
+    rstd = (z64.var(1, unbiased=False) + 1e-5).rsqrt()
+    # rstd: half the variance's error (48 additions of squares and the
+    # squares' own), its root and its quotient
+    assert ((out["rstd"].cpu().double() / rstd - 1).abs() <= 28 * 2.0 ** -24).all()
