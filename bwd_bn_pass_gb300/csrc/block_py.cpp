@@ -1,0 +1,484 @@
+// Python entry points of the backbone-block operators (GroupNorm, dropout,
+// LayerNorm with the drawn mask, rotary positions): argument checks, missing
+// outputs and workspaces, and the C call of gbnorm.h, for the functions of the
+// same purpose in gbnorm.py, which name and document the arguments.
+//
+// Why native: the small calls of these operators take the GPU 4 to 15 us, and a
+// marshalling in Python (13 us of attribute reads, conversions and allocations
+// for six tensors, besides 4 to 6 us of launch) was what they waited for.  The
+// checks here read the tensors directly and cost a few hundred nanoseconds in
+// all.
+//
+// Arguments are positional; tensors that may be missing are None.  Refusals
+// raise ValueError or TypeError before anything is launched, a nonzero status
+// of the C call raises the error class given to set_error.
+#include <Python.h>
+
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "gbnorm.h"
+
+namespace {
+
+using at::Tensor;
+
+PyObject* error_class = nullptr;
+
+[[noreturn]] void refuse(const char* name, const char* what) {
+  TORCH_CHECK_VALUE(false, name, " ", what);
+  __builtin_unreachable();
+}
+
+bool given(PyObject* o) { return o != Py_None; }
+
+// A CUDA tensor; contiguous unless its strides are passed on.
+const Tensor& cuda(PyObject* o, const char* name, bool strided = false) {
+  if (!THPVariable_Check(o)) refuse(name, "must be a CUDA tensor");
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda()) refuse(name, "must be a CUDA tensor");
+  if (!strided && !t.is_contiguous()) refuse(name, "must be contiguous");
+  return t;
+}
+
+int code(const Tensor& t) {
+  if (t.scalar_type() == at::kFloat) return GBN_F32;
+  if (t.scalar_type() == at::kBFloat16) return GBN_BF16;
+  TORCH_CHECK_TYPE(false, "unsupported dtype ", t.dtype(), "; use float32 or bfloat16");
+}
+
+int64_t integer(PyObject* o, const char* name) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    TORCH_CHECK_TYPE(false, name, " must be an integer");
+  }
+  return v;
+}
+
+double number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    TORCH_CHECK_TYPE(false, name, " must be a number");
+  }
+  return v;
+}
+
+bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+
+// The tensors of a call: all on the first one's device.
+struct Args {
+  const Tensor& ref;
+  explicit Args(const Tensor& r) : ref(r) {}
+
+  const Tensor& on(const Tensor& t, const char* name) const {
+    TORCH_CHECK_VALUE(t.get_device() == ref.get_device(), name, " is on ", t.device(),
+                      ", expected ", ref.device());
+    return t;
+  }
+  const Tensor& contiguous(PyObject* o, const char* name) const { return on(cuda(o, name), name); }
+  // of the reference's shape
+  const Tensor& like(PyObject* o, const char* name, at::ScalarType dt) const {
+    const Tensor& t = contiguous(o, name);
+    if (t.sizes() != ref.sizes() || t.scalar_type() != dt)
+      refuse(name, "must match in shape and dtype");
+    return t;
+  }
+  const Tensor& like(PyObject* o, const char* name) const { return like(o, name, ref.scalar_type()); }
+  // n values of the reference's dtype
+  const Tensor& vec(PyObject* o, const char* name, int64_t n) const {
+    const Tensor& t = contiguous(o, name);
+    if (t.scalar_type() != ref.scalar_type() || t.numel() != n)
+      refuse(name, "must match the rows' dtype and last dimension");
+    return t;
+  }
+  // n fp32 values (a statistics tensor of another type is rejected, never
+  // reinterpreted)
+  const Tensor& f32(PyObject* o, const char* name, int64_t n) const {
+    const Tensor& t = contiguous(o, name);
+    TORCH_CHECK_TYPE(t.scalar_type() == at::kFloat, name, " must be float32, got ", t.dtype());
+    TORCH_CHECK_VALUE(t.numel() == n, name, " must have ", n, " elements");
+    return t;
+  }
+  Tensor make(at::IntArrayRef sizes, at::ScalarType dt) const {
+    return at::empty(sizes, ref.options().dtype(dt));
+  }
+  Tensor make(at::IntArrayRef sizes) const { return at::empty(sizes, ref.options()); }
+  // the given workspace, or a new one of at least `bytes`
+  Tensor work(PyObject* o, size_t bytes) const {
+    if (given(o)) return contiguous(o, "ws");
+    return make({(int64_t)(bytes > 256 ? bytes : 256)}, at::kByte);
+  }
+  void* stream() const {
+    return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)ref.get_device()).stream();
+  }
+};
+
+void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+float* fptr(const Tensor& t) { return static_cast<float*>(ptr(t)); }
+
+// A vector that may be None: undefined then.
+Tensor vec_or_none(const Args& a, PyObject* o, const char* name, int64_t n) {
+  return given(o) ? a.vec(o, name, n) : Tensor();
+}
+Tensor f32_or_none(const Args& a, PyObject* o, const char* name, int64_t n) {
+  return given(o) ? a.f32(o, name, n) : Tensor();
+}
+
+PyObject* wrap(const Tensor& t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+
+template <typename... Ts>
+PyObject* result(int status, const char* fn, const Ts&... ts) {
+  if (status != GBN_OK) {
+    PyObject* e = PyObject_CallFunction(error_class, "si", fn, status);
+    if (e != nullptr) {
+      PyErr_SetObject(error_class, e);
+      Py_DECREF(e);
+    }
+    return nullptr;
+  }
+  if constexpr (sizeof...(Ts) == 1) {
+    return wrap(ts...);
+  } else {
+    PyObject* out = PyTuple_New(sizeof...(Ts));
+    if (out == nullptr) return nullptr;
+    Py_ssize_t i = 0;
+    (PyTuple_SET_ITEM(out, i++, wrap(ts)), ...);
+    return out;
+  }
+}
+
+// rows [R, H] of a contiguous tensor
+struct Rows {
+  int64_t R, H;
+};
+Rows rows_of(const Tensor& t, const char* name) {
+  if (t.dim() < 1) refuse(name, "must have a last (normalised) dimension");
+  const int64_t H = t.size(-1);
+  return {H ? t.numel() / H : 0, H};
+}
+
+// (seed, offset) as numbers modulo 2^64, or as two words on the device
+struct Rng {
+  uint64_t seed = 0, offset = 0;
+  const uint64_t* state = nullptr;
+  Rng(const Args& a, PyObject* o) {
+    if (THPVariable_Check(o)) {
+      const Tensor& t = cuda(o, "rng");
+      TORCH_CHECK_TYPE(t.scalar_type() == at::kLong && t.numel() == 2,
+                       "rng must be an int64 tensor (seed, offset) or a pair of ints");
+      state = static_cast<const uint64_t*>(a.on(t, "rng").data_ptr());
+      return;
+    }
+    uint64_t v[2];
+    TORCH_CHECK_TYPE(PySequence_Check(o) && PySequence_Size(o) == 2,
+                     "rng must be an int64 tensor (seed, offset) or a pair of ints");
+    for (int i = 0; i < 2; ++i) {
+      PyObject* item = PySequence_GetItem(o, i);
+      PyObject* n = item != nullptr ? PyNumber_Index(item) : nullptr;
+      Py_XDECREF(item);
+      if (n == nullptr) {
+        PyErr_Clear();
+        TORCH_CHECK_TYPE(false, "rng must be an int64 tensor (seed, offset) or a pair of ints");
+      }
+      v[i] = PyLong_AsUnsignedLongLongMask(n);
+      Py_DECREF(n);
+    }
+    seed = v[0], offset = v[1];
+  }
+};
+
+// ------------------------------------------- GroupNorm, channels last --
+
+struct GnDims {
+  int64_t N, S, C, G;
+};
+GnDims gn_dims(const Tensor& x, int64_t groups) {
+  TORCH_CHECK_VALUE(x.dim() >= 2,
+                    "channels-last GroupNorm wants a contiguous [N, ..., C] tensor");
+  const int64_t N = x.size(0), C = x.size(-1);
+  TORCH_CHECK_VALUE(groups >= 1 && C % groups == 0, groups, " groups do not divide ", C,
+                    " channels");
+  int64_t S = 1;
+  for (int64_t d = 1; d < x.dim() - 1; ++d) S *= x.size(d);
+  return {N, S, C, groups};
+}
+
+// x, groups, gamma, beta, eps, act, slope, y, stats, ws
+PyObject* gn_forward(PyObject* const* p) {
+  const Args a(cuda(p[0], "x"));
+  const Tensor& x = a.ref;
+  const GnDims d = gn_dims(x, integer(p[1], "groups"));
+  const int dt = code(x);
+  const Tensor gamma = f32_or_none(a, p[2], "gamma", d.C), beta = f32_or_none(a, p[3], "beta", d.C);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Tensor y = given(p[7]) ? a.like(p[7], "y") : a.make(x.sizes());
+  const Tensor stats = given(p[8]) ? a.f32(p[8], "stats", 3 * d.N * d.G)
+                                   : a.make({3, d.N, d.G}, at::kFloat);
+  const Tensor ws = a.work(p[9], given(p[9]) ? 0 : gbn_gn_nhwc_workspace_bytes(
+                                                       d.N, d.S, d.C, d.G, x.get_device()));
+  const int st = gbn_gn_nhwc_forward_train(
+      ptr(x), dt, d.N, d.S, d.C, d.G, fptr(gamma), fptr(beta), (float)number(p[4], "eps"),
+      (int)integer(p[5], "act"), (float)number(p[6], "slope"), ptr(y), fptr(stats), ptr(ws),
+      ws.nbytes(), a.stream());
+  return result(st, "gbn_gn_nhwc_forward_train", y, stats);
+}
+
+// x, dy, stats, gamma, beta, act, slope, dx, dgamma, dbeta, ws
+PyObject* gn_backward(PyObject* const* p) {
+  const Args a(cuda(p[0], "x"));
+  const Tensor& x = a.ref;
+  const Tensor& stats = a.contiguous(p[2], "stats");
+  TORCH_CHECK_VALUE(stats.dim() == 3 && stats.size(0) == 3,
+                    "stats must be the forward's [3, N, groups] tensor");
+  const GnDims d = gn_dims(x, stats.size(2));
+  a.f32(p[2], "stats", 3 * d.N * d.G);
+  const int dt = code(x);
+  const Tensor& dy = a.like(p[1], "dy");
+  const Tensor gamma = f32_or_none(a, p[3], "gamma", d.C), beta = f32_or_none(a, p[4], "beta", d.C);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Tensor dx = given(p[7]) ? a.like(p[7], "dx") : a.make(x.sizes());
+  const Tensor dgamma = given(p[8]) ? a.f32(p[8], "dgamma", d.C) : a.make({d.C}, at::kFloat);
+  const Tensor dbeta = given(p[9]) ? a.f32(p[9], "dbeta", d.C) : a.make({d.C}, at::kFloat);
+  const Tensor ws = a.work(p[10], given(p[10]) ? 0 : gbn_gn_nhwc_workspace_bytes(
+                                                         d.N, d.S, d.C, d.G, x.get_device()));
+  const int st = gbn_gn_nhwc_backward(
+      ptr(x), ptr(dy), dt, d.N, d.S, d.C, d.G, fptr(stats), fptr(gamma), fptr(beta),
+      (int)integer(p[5], "act"), (float)number(p[6], "slope"), ptr(dx), fptr(dgamma), fptr(dbeta),
+      ptr(ws), ws.nbytes(), a.stream());
+  return result(st, "gbn_gn_nhwc_backward", dx, dgamma, dbeta);
+}
+
+// ------------------------------------- head RMSNorm and rotary positions --
+
+// [T, H, D] with a contiguous last dimension; any token and head strides
+const Tensor& head_rows(const Tensor& t, const char* name) {
+  TORCH_CHECK_VALUE(t.dim() == 3 && (t.size(2) <= 1 || t.stride(2) == 1), name,
+                    " must be [tokens, heads, D] with a contiguous last dimension");
+  return t;
+}
+const Tensor& head_rows_like(const Args& a, PyObject* o, const char* name) {
+  const Tensor& t = head_rows(a.on(cuda(o, name, true), name), name);
+  if (t.sizes() != a.ref.sizes() || t.scalar_type() != a.ref.scalar_type())
+    refuse(name, "must match in shape and dtype");
+  return t;
+}
+
+struct Rope {
+  int64_t T, H, hq, D, rot;
+  int bits;
+  const Tensor& positions;
+  const Tensor& freqs;
+  Tensor wq, wk;
+  Rope(const Args& a, PyObject* pos, PyObject* fr, PyObject* q, PyObject* k, PyObject* q_heads)
+      : T(a.ref.size(0)), H(a.ref.size(1)), hq(given(q_heads) ? integer(q_heads, "q_heads") : H),
+        D(a.ref.size(2)), positions(a.contiguous(pos, "positions")),
+        freqs(a.contiguous(fr, "freqs")), wq(vec_or_none(a, q, "wq", D)),
+        wk(vec_or_none(a, k, "wk", D)) {
+    const auto pt = positions.scalar_type();
+    TORCH_CHECK_TYPE(pt == at::kInt || pt == at::kLong, "positions must be int32 or int64");
+    if (positions.numel() != T) refuse("positions", "must have one value per token");
+    TORCH_CHECK_TYPE(freqs.scalar_type() == at::kLong,
+                     "freqs must be the table of rope_frequencies");
+    bits = pt == at::kLong ? 64 : 32;
+    rot = 2 * freqs.numel();
+    if (!wq.defined()) wk = Tensor();
+    else TORCH_CHECK_VALUE(wk.defined() || hq >= H, "heads from q_heads on need wk");
+  }
+  const uint64_t* table() const { return static_cast<const uint64_t*>(freqs.data_ptr()); }
+};
+
+// x, positions, freqs, wq, wk, q_heads, eps, layout, scale, y, rstd, want_rstd
+PyObject* rope_forward(PyObject* const* p) {
+  const Args a(head_rows(cuda(p[0], "x", true), "x"));
+  const Tensor& x = a.ref;
+  const int dt = code(x);
+  const Rope r(a, p[1], p[2], p[3], p[4], p[5]);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Tensor y = given(p[9]) ? head_rows_like(a, p[9], "y") : a.make({r.T, r.H, r.D});
+  Tensor rstd;
+  if (r.wq.defined()) {
+    if (given(p[10])) rstd = a.f32(p[10], "rstd", r.T * r.H);
+    else if (truth(p[11])) rstd = a.make({r.T, r.H}, at::kFloat);
+  }
+  const int st = gbn_norm_rope_forward(
+      ptr(x), dt, r.T, r.H, r.hq, r.D, x.stride(0), x.stride(1), ptr(r.positions), r.bits,
+      r.table(), r.rot, (int)integer(p[7], "layout"), (float)number(p[8], "scale"), ptr(r.wq),
+      ptr(r.wk), (float)number(p[6], "eps"), ptr(y), y.stride(0), y.stride(1), fptr(rstd),
+      a.stream());
+  return result(st, "gbn_norm_rope_forward", y, rstd);
+}
+
+// dy, x, positions, freqs, rstd, wq, wk, q_heads, layout, scale, dx, dwq, dwk, ws
+PyObject* rope_backward(PyObject* const* p) {
+  const Args a(head_rows(cuda(p[0], "dy", true), "dy"));
+  const Tensor& dy = a.ref;
+  const int dt = code(dy);
+  const Rope r(a, p[2], p[3], p[5], p[6], p[7]);
+  const c10::cuda::CUDAGuard guard(dy.device());
+  Tensor x, rstd, dwq, dwk, ws;
+  if (r.wq.defined()) {
+    x = head_rows_like(a, p[1], "x");
+    if (!given(p[4])) refuse("rstd", "is required with a norm");
+    rstd = a.f32(p[4], "rstd", r.T * r.H);
+    dwq = given(p[11]) ? a.vec(p[11], "dwq", r.D) : a.make(r.wq.sizes());
+    if (given(p[12])) dwk = a.vec(p[12], "dwk", r.D);
+    else if (r.wk.defined()) dwk = a.make(r.wk.sizes());
+    ws = a.work(p[13], given(p[13]) ? 0 : gbn_norm_rope_workspace_bytes(
+                                              r.T, r.H, r.hq, r.D, r.rot, dt, dy.get_device()));
+  } else {
+    TORCH_CHECK_VALUE(!given(p[11]) && !given(p[12]), "weight gradients without weights");
+  }
+  const Tensor dx = given(p[10]) ? head_rows_like(a, p[10], "dx") : a.make({r.T, r.H, r.D});
+  const int st = gbn_norm_rope_backward(
+      ptr(dy), ptr(x), dt, r.T, r.H, r.hq, r.D, dy.stride(0), dy.stride(1),
+      x.defined() ? x.stride(0) : 0, x.defined() ? x.stride(1) : 0, ptr(r.positions), r.bits,
+      r.table(), r.rot, (int)integer(p[8], "layout"), (float)number(p[9], "scale"), fptr(rstd),
+      ptr(r.wq), ptr(r.wk), ptr(dx), dx.stride(0), dx.stride(1), ptr(dwq), ptr(dwk), ptr(ws),
+      ws.defined() ? ws.nbytes() : 0, a.stream());
+  return result(st, "gbn_norm_rope_backward", dx, dwq, dwk);
+}
+
+// ------------------------------------------- dropout, mask never stored --
+
+// x, p, rng, bias, residual, y
+PyObject* dropout_forward(PyObject* const* p) {
+  const Args a(cuda(p[0], "x"));
+  const Tensor& x = a.ref;
+  const Rows d = rows_of(x, "x");
+  const int dt = code(x);
+  const Tensor bias = vec_or_none(a, p[3], "bias", d.H);
+  const Tensor residual = given(p[4]) ? a.like(p[4], "residual") : Tensor();
+  const Rng rng(a, p[2]);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Tensor y = given(p[5]) ? a.like(p[5], "y") : a.make(x.sizes());
+  const int st = gbn_dropout_forward(ptr(x), dt, d.R, d.H, ptr(bias), ptr(residual),
+                                     number(p[1], "p"), rng.seed, rng.offset, rng.state, ptr(y),
+                                     a.stream());
+  return result(st, "gbn_dropout_forward", y);
+}
+
+// dy, p, rng, want_dbias, dx, dbias, ws
+PyObject* dropout_backward(PyObject* const* p) {
+  const Args a(cuda(p[0], "dy"));
+  const Tensor& dy = a.ref;
+  const Rows d = rows_of(dy, "dy");
+  const int dt = code(dy);
+  const Rng rng(a, p[2]);
+  const c10::cuda::CUDAGuard guard(dy.device());
+  const Tensor dx = given(p[4]) ? a.like(p[4], "dx") : a.make(dy.sizes());
+  Tensor dbias, ws;
+  if (given(p[5])) dbias = a.vec(p[5], "dbias", d.H);
+  else if (truth(p[3])) dbias = a.make({d.H});
+  if (dbias.defined())
+    ws = a.work(p[6], given(p[6]) ? 0 : gbn_dropout_workspace_bytes(d.R, d.H, dt, dy.get_device()));
+  const int st = gbn_dropout_backward(ptr(dy), dt, d.R, d.H, number(p[1], "p"), rng.seed,
+                                      rng.offset, rng.state, ptr(dx), ptr(dbias), ptr(ws),
+                                      ws.defined() ? ws.nbytes() : 0, a.stream());
+  return result(st, "gbn_dropout_backward", dx, dbias);
+}
+
+// x, residual, p, rng, gamma, beta, eps, bias, y, z, mean, rstd, want_z
+PyObject* ln_forward(PyObject* const* p) {
+  const Args a(cuda(p[0], "x"));
+  const Tensor& x = a.ref;
+  const Rows d = rows_of(x, "x");
+  const int dt = code(x);
+  const Tensor& residual = a.like(p[1], "residual");
+  const Tensor gamma = vec_or_none(a, p[4], "gamma", d.H), beta = vec_or_none(a, p[5], "beta", d.H),
+               bias = vec_or_none(a, p[7], "bias", d.H);
+  const Rng rng(a, p[3]);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Tensor y = given(p[8]) ? a.like(p[8], "y") : a.make(x.sizes());
+  Tensor z;
+  if (given(p[9])) z = a.like(p[9], "z");
+  else if (truth(p[12])) z = a.make(x.sizes());
+  const Tensor mean = given(p[10]) ? a.f32(p[10], "mean", d.R) : a.make({d.R}, at::kFloat);
+  const Tensor rstd = given(p[11]) ? a.f32(p[11], "rstd", d.R) : a.make({d.R}, at::kFloat);
+  const int st = gbn_layernorm_dropout_forward(
+      ptr(x), dt, d.R, d.H, ptr(residual), ptr(bias), number(p[2], "p"), rng.seed, rng.offset,
+      rng.state, ptr(gamma), ptr(beta), (float)number(p[6], "eps"), ptr(y), ptr(z), fptr(mean),
+      fptr(rstd), a.stream());
+  return result(st, "gbn_layernorm_dropout_forward", y, z, mean, rstd);
+}
+
+// dy, x, residual, mean, rstd, gamma, p, rng, bias, dz_extra, dx, dresidual, dgamma, dbeta, dbias,
+// ws, want_dbias, saved_z, dres_f32
+PyObject* ln_backward(PyObject* const* p) {
+  const Args a(cuda(p[1], "x"));
+  const Tensor& x = a.ref;
+  const Rows d = rows_of(x, "x");
+  const int dt = code(x);
+  const bool saved_z = truth(p[17]), dres_f32 = truth(p[18]);
+  const Tensor& dy = a.like(p[0], "dy");
+  TORCH_CHECK_VALUE(given(p[2]) || saved_z,
+                    "residual is required (or saved_z, with x the saved z)");
+  const Tensor residual = given(p[2]) ? a.like(p[2], "residual") : Tensor();
+  const Tensor& mean = a.f32(p[3], "mean", d.R);
+  const Tensor& rstd = a.f32(p[4], "rstd", d.R);
+  const Tensor& gamma = a.vec(p[5], "gamma", d.H);
+  const Tensor bias = vec_or_none(a, p[8], "bias", d.H);
+  const Tensor extra = f32_or_none(a, p[9], "dz_extra", x.numel());
+  const Rng rng(a, p[7]);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const at::ScalarType rt = dres_f32 ? at::kFloat : x.scalar_type();
+  const Tensor dx = given(p[10]) ? a.like(p[10], "dx") : a.make(x.sizes());
+  const Tensor dres = given(p[11]) ? a.like(p[11], "dresidual", rt) : a.make(x.sizes(), rt);
+  const Tensor dgamma = given(p[12]) ? a.vec(p[12], "dgamma", d.H) : a.make(gamma.sizes());
+  const Tensor dbeta = given(p[13]) ? a.vec(p[13], "dbeta", d.H) : a.make(gamma.sizes());
+  Tensor dbias;
+  if (given(p[14])) dbias = a.vec(p[14], "dbias", d.H);
+  else if (truth(p[16])) dbias = a.make(gamma.sizes());
+  const Tensor ws = a.work(p[15], given(p[15]) ? 0 : gbn_rowwise_workspace_bytes(
+                                                         d.R, d.H, GBN_ROW_LN_FUSED, dt,
+                                                         x.get_device()));
+  const int flags = (saved_z ? GBN_LN_SAVED_Z : 0) | (dres_f32 ? GBN_LN_DRES_F32 : 0);
+  const int st = gbn_layernorm_dropout_backward(
+      ptr(dy), ptr(x), dt, fptr(mean), fptr(rstd), ptr(gamma), d.R, d.H, ptr(residual), ptr(bias),
+      number(p[6], "p"), rng.seed, rng.offset, rng.state, fptr(extra), ptr(dx), ptr(dres),
+      ptr(dgamma), ptr(dbeta), ptr(dbias), ptr(ws), ws.nbytes(), flags, a.stream());
+  return result(st, "gbn_layernorm_dropout_backward", dx, dres, dgamma, dbeta, dbias);
+}
+
+template <PyObject* (*F)(PyObject* const*), int COUNT>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != COUNT) {
+    PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", COUNT, count);
+    return nullptr;
+  }
+  return F(args);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* set_error(PyObject*, PyObject* cls) {
+  Py_INCREF(cls);
+  Py_XSETREF(error_class, cls);
+  Py_RETURN_NONE;
+}
+
+#define GBN_ENTRY(name, count) \
+  {#name, (PyCFunction)(void (*)(void))entry<name, count>, METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {GBN_ENTRY(gn_forward, 10),
+                         GBN_ENTRY(gn_backward, 11),
+                         GBN_ENTRY(rope_forward, 12),
+                         GBN_ENTRY(rope_backward, 14),
+                         GBN_ENTRY(dropout_forward, 6),
+                         GBN_ENTRY(dropout_backward, 7),
+                         GBN_ENTRY(ln_forward, 13),
+                         GBN_ENTRY(ln_backward, 19),
+                         {"set_error", set_error, METH_O, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__block() { return PyModule_Create(&module); }

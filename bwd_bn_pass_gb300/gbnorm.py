@@ -9,7 +9,6 @@ call fails, an exception is raised.
 """
 
 import ctypes
-import functools
 import math
 import os
 
@@ -167,35 +166,28 @@ def _check(fn, status):
         raise GbnError(fn, status)
 
 
-def _call(device, name, *args):
-    """Call an entry point whose last argument is the stream, with ``device``
-    current; raise on a nonzero status.  (The current device is switched only
-    where it is another one: the switch costs more than a small kernel.)"""
-    fn = _entry.get(name)
-    if fn is None:
-        fn = _entry[name] = getattr(lib(), name)
-    index = device.index
-    if index == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if st != GBN_OK:
-        raise GbnError(name, st)
+def _native():
+    """The module that marshals the backbone-block calls (built next to the
+    library; csrc/block_py.cpp).  Raises ImportError if it is not built."""
+    global _block
+    if _block is None:
+        lib()
+        if not os.path.exists(_build.module_path()):
+            raise ImportError(
+                f"{_build.module_path()} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        from . import _block as module
+        module.set_error(GbnError)
+        _block = module
+    return _block
 
 
-_entry = {}  # entry points by name
-
-
-@functools.lru_cache(maxsize=4096)
-def _ws_bytes(name, device_index, *args):
-    """A workspace size query (a function of the shape and the device)."""
-    return int(getattr(lib(), name)(*args, device_index))
+_block = None
 
 
 def _workspace(name, device, *args):
-    n = _ws_bytes(name, device.index, *args)
-    return torch.empty(n if n > 256 else 256, dtype=torch.uint8, device=device)
+    n = int(getattr(lib(), name)(*args, device.index))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
 def _cuda(t, name):
@@ -763,22 +755,8 @@ def gn_nhwc_forward_train(x, groups, gamma=None, beta=None, eps=1e-5, *, act=Non
     contiguous [N, ..., C] tensor, the groups are runs of C / groups adjacent
     channels.  Returns (y, stats) with stats fp32 [3, N, groups] = (mean, rstd,
     the mean's remainder)."""
-    code = _gn_act(act)
-    N, S, C = _gn_dims(x, groups)
-    _fp32_vec(gamma, "gamma", C)
-    _fp32_vec(beta, "beta", C)
-    y = torch.empty_like(x) if y is None else _like(y, x, "y")
-    if stats is None:
-        stats = torch.empty(3, N, groups, dtype=torch.float32, device=x.device)
-    else:
-        _fp32_vec(stats, "stats", 3 * N * groups)
-    if ws is None:
-        ws = _workspace("gbn_gn_nhwc_workspace_bytes", x.device, N, S, C, groups)
-    _same_device(x, ("y", y), ("stats", stats), ("ws", ws), ("gamma", gamma), ("beta", beta))
-    _call(x.device, "gbn_gn_nhwc_forward_train", _ptr(x), _code(x.dtype), N, S, C, groups,
-          _ptr(gamma), _ptr(beta), float(eps), code, float(slope), _ptr(y), _ptr(stats),
-          _ptr(ws), ws.numel() * ws.element_size())
-    return y, stats
+    return (_block or _native()).gn_forward(x, groups, gamma, beta, eps, _gn_act(act), slope, y,
+                                            stats, ws)
 
 
 def gn_nhwc_backward(x, dy, stats, gamma=None, beta=None, *, act=None, slope=0.01, dx=None,
@@ -786,28 +764,8 @@ def gn_nhwc_backward(x, dy, stats, gamma=None, beta=None, *, act=None, slope=0.0
     """Backward of ``gn_nhwc_forward_train`` from its ``stats``, with the same
     gamma, beta, act and slope.  Returns (dx, dgamma, dbeta), the last two
     fp32 [C]."""
-    code = _gn_act(act)
-    if _cuda(stats, "stats").dim() != 3 or stats.shape[0] != 3:
-        raise ValueError("stats must be the forward's [3, N, groups] tensor")
-    groups = stats.shape[2]
-    N, S, C = _gn_dims(x, groups)
-    _fp32_vec(stats, "stats", 3 * N * groups)
-    _like(dy, x, "dy")
-    dx = torch.empty_like(x) if dx is None else _like(dx, x, "dx")
-    if dgamma is None:
-        dgamma = torch.empty(C, dtype=torch.float32, device=x.device)
-    if dbeta is None:
-        dbeta = torch.empty(C, dtype=torch.float32, device=x.device)
-    for name, t in (("gamma", gamma), ("beta", beta), ("dgamma", dgamma), ("dbeta", dbeta)):
-        _fp32_vec(t, name, C)
-    if ws is None:
-        ws = _workspace("gbn_gn_nhwc_workspace_bytes", x.device, N, S, C, groups)
-    _same_device(x, ("dy", dy), ("stats", stats), ("gamma", gamma), ("beta", beta), ("dx", dx),
-                 ("dgamma", dgamma), ("dbeta", dbeta), ("ws", ws))
-    _call(x.device, "gbn_gn_nhwc_backward", _ptr(x), _ptr(dy), _code(x.dtype), N, S, C, groups,
-          _ptr(stats), _ptr(gamma), _ptr(beta), code, float(slope), _ptr(dx), _ptr(dgamma),
-          _ptr(dbeta), _ptr(ws), ws.numel() * ws.element_size())
-    return dx, dgamma, dbeta
+    return (_block or _native()).gn_backward(x, dy, stats, gamma, beta, _gn_act(act), slope, dx,
+                                             dgamma, dbeta, ws)
 
 
 # ------------------------------------- head RMSNorm and rotary positions --
@@ -865,38 +823,10 @@ def rope_frequencies(inv_freq, device=None):
     return ((hi.to(torch.int64) << 32) | lo.to(torch.int64)).to(device or inv_freq.device)
 
 
-def _rope_rows(t, name, shape=None):
-    """A [T, H, D] CUDA tensor whose last dimension is contiguous; its token
-    and head strides."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [tokens, heads, D] with a contiguous last dimension")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    return t.stride(0), t.stride(1)
-
-
-def _rope_args(x, positions, freqs, wq, wk, q_heads, layout):
-    T, H, D = x.shape
-    q_heads = H if q_heads is None else int(q_heads)
+def _rope_layout(layout):
     if layout not in _ROPE_LAYOUTS:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    if _cuda(positions, "positions").dtype not in (torch.int32, torch.int64):
-        raise TypeError("positions must be int32 or int64")
-    if positions.numel() != T:
-        raise ValueError("positions must have one value per token")
-    if _cuda(freqs, "freqs").dtype != torch.int64:
-        raise TypeError("freqs must be the table of rope_frequencies")
-    for name, w in (("wq", wq), ("wk", wk)):
-        _col_vec(w, x, D, name)
-    if wq is None:
-        wk = None
-    elif wk is None and q_heads < H:
-        raise ValueError("heads from q_heads on need wk")
-    _same_device(x, ("positions", positions), ("freqs", freqs), ("wq", wq), ("wk", wk))
-    return (T, H, q_heads, D, 64 if positions.dtype == torch.int64 else 32, 2 * freqs.numel(),
-            _ROPE_LAYOUTS[layout], wk)
+    return _ROPE_LAYOUTS[layout]
 
 
 def norm_rope_forward(x, positions, freqs, wq=None, wk=None, *, q_heads=None, eps=1e-5,
@@ -910,23 +840,8 @@ def norm_rope_forward(x, positions, freqs, wq=None, wk=None, *, q_heads=None, ep
     Returns (y, rstd) -- y contiguous unless given (y=x turns in place), rstd
     fp32 [tokens, heads] for the backward, or None without a norm or with
     ``want_rstd=False``."""
-    xs = _rope_rows(x, "x")
-    T, H, hq, D, bits, rot, lay, wk = _rope_args(x, positions, freqs, wq, wk, q_heads, layout)
-    if y is None:
-        y = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    elif y.dtype != x.dtype:
-        raise ValueError("y must match x's dtype")
-    ys = _rope_rows(y, "y", x.shape)
-    if wq is None:
-        rstd = None
-    elif rstd is None and want_rstd:
-        rstd = torch.empty((T, H), dtype=torch.float32, device=x.device)
-    _fp32_vec(rstd, "rstd", T * H)
-    _same_device(x, ("y", y), ("rstd", rstd))
-    _call(x.device, "gbn_norm_rope_forward", _ptr(x), _code(x.dtype), T, H, hq, D, *xs,
-          _ptr(positions), bits, _ptr(freqs), rot, lay, float(scale), _ptr(wq), _ptr(wk),
-          float(eps), _ptr(y), *ys, _ptr(rstd))
-    return y, rstd
+    return (_block or _native()).rope_forward(x, positions, freqs, wq, wk, q_heads, eps,
+                                              _rope_layout(layout), scale, y, rstd, want_rstd)
 
 
 def norm_rope_workspace(x, q_heads, rot):
@@ -941,77 +856,18 @@ def norm_rope_backward(dy, x, positions, freqs, rstd=None, wq=None, wk=None, *, 
     ``rstd``.  Returns (dx, dwq, dwk): dx contiguous unless given (a slice of
     the packed gradient), dwq / dwk None where there is no such weight.
     Without ``wq``, x and rstd are not read (x may be None)."""
-    ds = _rope_rows(dy, "dy")
-    T, H, hq, D, bits, rot, lay, wk = _rope_args(dy, positions, freqs, wq, wk, q_heads, layout)
-    xs = (0, 0)
-    if wq is not None:
-        xs = _rope_rows(x, "x", dy.shape)
-        if x.dtype != dy.dtype:
-            raise ValueError("dy must match x's dtype")
-        if rstd is None:
-            raise ValueError("rstd is required with a norm")
-        _fp32_vec(rstd, "rstd", T * H)
-        dwq = torch.empty_like(wq) if dwq is None else dwq
-        dwk = torch.empty_like(wk) if dwk is None and wk is not None else dwk
-        _col_vec(dwq, dy, D, "dwq")
-        _col_vec(dwk, dy, D, "dwk")
-        ws = norm_rope_workspace(dy, hq, rot) if ws is None else _cuda(ws, "ws")
-    elif dwq is not None or dwk is not None:
-        raise ValueError("weight gradients without weights")
-    if dx is None:
-        dx = torch.empty((T, H, D), dtype=dy.dtype, device=dy.device)
-    elif dx.dtype != dy.dtype:
-        raise ValueError("dx must match dy's dtype")
-    os_ = _rope_rows(dx, "dx", dy.shape)
-    _same_device(dy, ("x", x), ("rstd", rstd), ("dx", dx), ("dwq", dwq), ("dwk", dwk), ("ws", ws))
-    _call(dy.device, "gbn_norm_rope_backward", _ptr(dy), _ptr(x), _code(dy.dtype), T, H, hq, D,
-          *ds, *xs, _ptr(positions), bits, _ptr(freqs), rot, lay, float(scale), _ptr(rstd),
-          _ptr(wq), _ptr(wk), _ptr(dx), *os_, _ptr(dwq), _ptr(dwk), _ptr(ws), 0 if ws is
-          None else ws.numel() * ws.element_size())
-    return dx, dwq, dwk
+    return (_block or _native()).rope_backward(dy, x, positions, freqs, rstd, wq, wk, q_heads,
+                                               _rope_layout(layout), scale, dx, dwq, dwk, ws)
 
 
 # ------------------------------------------- dropout, mask never stored --
-
-def _rng(rng, ref):
-    """(seed, offset, rng_state) of a dropout call: ``rng`` is a pair of
-    Python ints (taken modulo 2**64), or a CUDA int64 tensor of two elements
-    (seed, offset) that the kernels read when they run."""
-    if isinstance(rng, torch.Tensor):
-        if _cuda(rng, "rng").dtype != torch.int64 or rng.numel() != 2:
-            raise TypeError("rng must be an int64 tensor (seed, offset) or a pair of ints")
-        _same_device(ref, ("rng", rng))
-        return 0, 0, _ptr(rng)
-    seed, offset = rng
-    return int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFFFFFFFFFF, None
-
-
-def _like(t, ref, name):
-    if _cuda(t, name).shape != ref.shape or t.dtype != ref.dtype:
-        raise ValueError(f"{name} must match in shape and dtype")
-    return t
-
-
-def _col_vec(t, ref, H, name):
-    if t is not None and (_cuda(t, name).dtype != ref.dtype or t.numel() != H):
-        raise ValueError(f"{name} must match the rows' dtype and last dimension")
-
 
 def dropout_forward(x, p, rng, *, bias=None, residual=None, y=None):
     """``y = residual + keep*s*(x + bias)`` over the rows of a contiguous
     [..., H] tensor; the mask comes from the counter-based generator of
     ``rng`` = (seed, offset) (see gbn_dropout_forward) and is not stored.
     The backward draws it again from the same ``rng``."""
-    R, H = _rows(x, "x")
-    _col_vec(bias, x, H, "bias")
-    if residual is not None:
-        _like(residual, x, "residual")
-    y = torch.empty_like(x) if y is None else _like(y, x, "y")
-    _same_device(x, ("bias", bias), ("residual", residual), ("y", y))
-    seed, offset, state = _rng(rng, x)
-    _call(x.device, "gbn_dropout_forward", _ptr(x), _code(x.dtype), R, H, _ptr(bias),
-          _ptr(residual), float(p), seed, offset, state, _ptr(y))
-    return y
+    return (_block or _native()).dropout_forward(x, p, rng, bias, residual, y)
 
 
 def dropout_workspace(dy):
@@ -1023,19 +879,7 @@ def dropout_backward(dy, p, rng, *, want_dbias=False, dx=None, dbias=None, ws=No
     """Backward of ``dropout_forward`` for the same ``p`` and ``rng``.
     Returns (dx, dbias); dbias is None unless wanted (or given).  The
     residual's gradient is dy itself."""
-    R, H = _rows(dy, "dy")
-    dx = torch.empty_like(dy) if dx is None else _like(dx, dy, "dx")
-    if dbias is None and want_dbias:
-        dbias = torch.empty(H, dtype=dy.dtype, device=dy.device)
-    _col_vec(dbias, dy, H, "dbias")
-    if dbias is not None and ws is None:
-        ws = dropout_workspace(dy)
-    _same_device(dy, ("dx", dx), ("dbias", dbias), ("ws", ws))
-    seed, offset, state = _rng(rng, dy)
-    _call(dy.device, "gbn_dropout_backward", _ptr(dy), _code(dy.dtype), R, H, float(p), seed,
-          offset, state, _ptr(dx), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel() *
-          ws.element_size())
-    return dx, dbias
+    return (_block or _native()).dropout_backward(dy, p, rng, want_dbias, dx, dbias, ws)
 
 
 def layernorm_dropout_forward(x, residual, p, rng, gamma=None, beta=None, eps=1e-5, *, bias=None,
@@ -1044,26 +888,8 @@ def layernorm_dropout_forward(x, residual, p, rng, gamma=None, beta=None, eps=1e
     ``rng`` (see ``dropout_forward``): z = residual + keep*s*(x + bias), y =
     LayerNorm(z).  Returns a dict with y, z (None when not wanted), mean,
     rstd."""
-    R, H = _rows(x, "x")
-    _like(residual, x, "residual")
-    for name, t in (("gamma", gamma), ("beta", beta), ("bias", bias)):
-        _col_vec(t, x, H, name)
-    y = torch.empty_like(x) if y is None else _like(y, x, "y")
-    if z is None and want_z:
-        z = torch.empty_like(x)
-    if z is not None:
-        _like(z, x, "z")
-    mean = torch.empty(R, dtype=torch.float32, device=x.device) if mean is None else mean
-    rstd = torch.empty(R, dtype=torch.float32, device=x.device) if rstd is None else rstd
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if _cuda(t, name).dtype != torch.float32 or t.numel() != R:
-            raise TypeError(f"{name} must be float32 with one value per row")
-    _same_device(x, ("residual", residual), ("gamma", gamma), ("beta", beta), ("bias", bias),
-                 ("y", y), ("z", z), ("mean", mean), ("rstd", rstd))
-    seed, offset, state = _rng(rng, x)
-    _call(x.device, "gbn_layernorm_dropout_forward", _ptr(x), _code(x.dtype), R, H,
-          _ptr(residual), _ptr(bias), float(p), seed, offset, state, _ptr(gamma),
-          _ptr(beta), float(eps), _ptr(y), _ptr(z), _ptr(mean), _ptr(rstd))
+    y, z, mean, rstd = (_block or _native()).ln_forward(
+        x, residual, p, rng, gamma, beta, eps, bias, y, z, mean, rstd, want_z)
     return {"y": y, "z": z, "mean": mean, "rstd": rstd}
 
 
@@ -1076,42 +902,7 @@ def layernorm_dropout_backward(dy, x, residual, mean, rstd, gamma, p, rng, *, bi
     ``bias``) None.  ``dz_extra`` and ``dres_f32`` as in
     ``layernorm_backward``.  Returns a dict with dx, dresidual, dgamma, dbeta,
     dbias."""
-    R, H = _rows(x, "x")
-    _like(dy, x, "dy")
-    if residual is not None:
-        _like(residual, x, "residual")
-    elif not saved_z:
-        raise ValueError("residual is required (or saved_z, with x the saved z)")
-    for name, t in (("gamma", gamma), ("bias", bias), ("dgamma", dgamma), ("dbeta", dbeta),
-                    ("dbias", dbias)):
-        _col_vec(t, x, H, name)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if _cuda(t, name).dtype != torch.float32 or t.numel() != R:
-            raise TypeError(f"{name} must be float32 with one value per row")
-    if dz_extra is not None and (_cuda(dz_extra, "dz_extra").dtype != torch.float32
-                                 or dz_extra.numel() != x.numel()):
-        raise TypeError("dz_extra must be float32, one value per element")
-    res_dtype = torch.float32 if dres_f32 else x.dtype
-    dx = torch.empty_like(x) if dx is None else _like(dx, x, "dx")
-    if dresidual is None:
-        dresidual = torch.empty_like(x, dtype=res_dtype)
-    elif _cuda(dresidual, "dresidual").shape != x.shape or dresidual.dtype != res_dtype:
-        raise ValueError("dresidual must match x (float32 with dres_f32)")
-    dgamma = torch.empty_like(gamma) if dgamma is None else dgamma
-    dbeta = torch.empty_like(gamma) if dbeta is None else dbeta
-    if dbias is None and want_dbias:
-        dbias = torch.empty_like(gamma)
-    if ws is None:
-        ws = _workspace("gbn_rowwise_workspace_bytes", x.device, R, H, GBN_ROW_LN_FUSED,
-                        _code(x.dtype))
-    _same_device(x, ("dy", dy), ("residual", residual), ("mean", mean), ("rstd", rstd),
-                 ("gamma", gamma), ("bias", bias), ("dz_extra", dz_extra), ("dx", dx),
-                 ("dresidual", dresidual), ("dgamma", dgamma), ("dbeta", dbeta),
-                 ("dbias", dbias), ("ws", ws))
-    seed, offset, state = _rng(rng, x)
-    flags = (GBN_LN_SAVED_Z if saved_z else 0) | (GBN_LN_DRES_F32 if dres_f32 else 0)
-    _call(x.device, "gbn_layernorm_dropout_backward", _ptr(dy), _ptr(x), _code(x.dtype),
-          _ptr(mean), _ptr(rstd), _ptr(gamma), R, H, _ptr(residual), _ptr(bias), float(p),
-          seed, offset, state, _ptr(dz_extra), _ptr(dx), _ptr(dresidual), _ptr(dgamma),
-          _ptr(dbeta), _ptr(dbias), _ptr(ws), ws.numel() * ws.element_size(), flags)
+    dx, dresidual, dgamma, dbeta, dbias = (_block or _native()).ln_backward(
+        dy, x, residual, mean, rstd, gamma, p, rng, bias, dz_extra, dx, dresidual, dgamma, dbeta,
+        dbias, ws, want_dbias, saved_z, dres_f32)
     return {"dx": dx, "dresidual": dresidual, "dgamma": dgamma, "dbeta": dbeta, "dbias": dbias}
