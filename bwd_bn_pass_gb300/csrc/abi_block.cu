@@ -306,11 +306,12 @@ int gbn_layernorm_dropout_forward(const void* input, int dtype, int64_t R, int64
   const DevInfo* dev = device_info(-1);
   if (!dev) return GBN_ECUDA;
   const int64_t esize = dtype == GBN_F32 ? 4 : 2;
-  const bool vec_ok = (H * esize) % 16 == 0 && aligned(input, 16) && aligned(residual, 16) &&
-                      aligned(bias, 16) && aligned(gamma, 16) && aligned(beta, 16) &&
-                      aligned(y, 16) && aligned(z, 16);
+  const bool rows = aligned(input, 16) && aligned(residual, 16) && aligned(y, 16) && aligned(z, 16);
+  const bool vec_ok = (H * esize) % 16 == 0 && rows && aligned(bias, 16) && aligned(gamma, 16) &&
+                      aligned(beta, 16);
   const RngArgs rng = make_rng(p, seed, offset, rng_state);
   RowFwdPtrs q;
+  q.rows_aligned = rows;
   q.x = input;
   q.residual = residual;
   q.bias = bias;

@@ -41,6 +41,7 @@
 #include "gbn_internal.h"
 #include "packed.cuh"
 #include "philox.cuh"
+#include "row_team.cuh"
 
 namespace gbn {
 
@@ -64,6 +65,7 @@ struct FwdArgs {
   int64_t R;
   int32_t H;
   int32_t Hv;            // 16-byte vectors per row (vector kernels)
+  int32_t team;          // a row team's threads (0: no teams)
   float eps;
   float scale;           // dropout scale
   RngArgs rng;           // kRowLnRng: the generator (its scale is `scale`)
@@ -515,6 +517,101 @@ __global__ void __launch_bounds__(128, kRngBlocks<KV>) row_fwd_rng_kernel(const 
   }
 }
 
+// The drawn mask for rows that are no whole vectors, up to kTeamMaxH elements of
+// aligned tensors: a team of threads per row (row_team.cuh), a chunk of the row a
+// thread, in registers through both statistics passes; bias, gamma and beta in
+// shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kTeamMaxThreads, 1) row_fwd_team_kernel(const FwdArgs a) {
+  extern __shared__ __align__(16) float par[];  // [bias, gamma, beta][8P]
+  __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  __shared__ float2 red[2][kTeamMaxThreads / 32];
+  const int H = a.H, P = team_pitch(H), n = 8 * P, TY = blockDim.x / a.team;
+  RowTeam team(red, a.team);
+  // the next row's chunk is loaded while this one is worked on
+  int64_t r = (int64_t)blockIdx.x * TY + team.team;
+  const int64_t step = (int64_t)gridDim.x * TY;
+  RowChunk next(r, a.R, H, team.tx);
+  Raw8<T> xr, rr;
+  auto load = [&] {
+    if (r < a.R && next.any()) {
+      xr.load(static_cast<const T*>(a.x) + next.at, next);
+      rr.load(static_cast<const T*>(a.res) + next.at, next);
+    }
+  };
+  load();
+  philox_fill(keys, a.rng);
+  for (int j = threadIdx.x; j < H; j += blockDim.x) {
+    const int w = column_word(j, P);
+    par[w] = a.bias != nullptr ? to_f32(static_cast<const T*>(a.bias)[j]) : 0.f;
+    par[n + w] = a.w != nullptr ? to_f32(static_cast<const T*>(a.w)[j]) : 1.f;
+    par[2 * n + w] = a.beta != nullptr ? to_f32(static_cast<const T*>(a.beta)[j]) : 0.f;
+  }
+  __syncthreads();
+  Philox<true> gen;
+  gen.load(a.rng, keys);
+  const float invH = 1.f / (float)H;
+  while (r < a.R) {
+    const RowChunk c = next;
+    const int64_t row = r;
+    float z[8];
+    float2 s = make_float2(0.f, 0.f);
+    if (c.any()) {
+      const uint32_t kept = gen.bits((uint64_t)c.at >> 3);
+      float rv[8];
+      xr.get(z);
+      rr.get(rv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (!c.has(e)) continue;
+        const float v = z[e] + par[c.word(e, team.tx, P)];
+        z[e] = fmaf((kept >> e) & 1u ? v : 0.f, a.scale, rv[e]);
+        s.x += z[e];
+      }
+    }
+    r += step;
+    next = RowChunk(r, a.R, H, team.tx);
+    load();
+    const float m = team.sum(s).x * invH;
+    if (a.z != nullptr && c.any()) chunk_store(static_cast<T*>(a.z) + c.at, z, c);
+    s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (!c.has(e)) continue;
+      z[e] -= m;
+      s.x += z[e];
+      s.y = fmaf(z[e], z[e], s.y);
+    }
+    s = team.sum(s);
+    const Centred f(m, s.x, s.y, invH, a.eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (!c.has(e)) continue;
+      const int w = c.word(e, team.tx, P);
+      z[e] = fmaf((z[e] - f.lack) * f.rstd, par[n + w], par[2 * n + w]);
+    }
+    if (c.any()) chunk_store(static_cast<T*>(a.y) + c.at, z, c);
+    if (team.tx == 0) {
+      a.mean[row] = f.mean;
+      a.rstd[row] = f.rstd;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_fwd_team(const FwdArgs& a, const DevInfo& dev, cudaStream_t st) {
+  const size_t smem = (size_t)3 * 8 * team_pitch(a.H) * sizeof(float);
+  // the longest rows alone need more than 512 threads; 64 registers a thread
+  int64_t ty = a.team <= 512 ? teams_of_block(a.team, 512) : 1;
+  const int64_t want = (a.R + 2 * dev.sms - 1) / (2 * dev.sms);
+  if (ty > want) ty = want;
+  const int nt = (int)ty * a.team;
+  const int64_t per_sm = 1024 / nt < 4 ? 1024 / nt : 4;
+  const int64_t blocks = (a.R + ty - 1) / ty, cap = (int64_t)dev.sms * per_sm;
+  return launch(row_fwd_team_kernel<T>, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(nt),
+                smem, st, false, a);
+}
+
 // Any H and alignment: block g owns rows g, g+G, ...; each pass walks the
 // row with stride blockDim (z is recomputed, the row is re-read from L2).
 template <typename T, int KIND>
@@ -603,6 +700,7 @@ cudaError_t launch_kind(const FwdArgs& a, bool vec_ok, const DevInfo& dev, cudaS
   const int64_t R = a.R;
   if constexpr (KIND == kRowLnRng) {
     if (vec_ok && a.Hv <= 256) return launch_rng<T, 8>(a, dev, st);
+    if (a.team != 0) return launch_fwd_team<T>(a, dev, st);
   } else if (vec_ok && a.Hv <= 256) {
     // one warp per row, 8 per block; z of each row in shared memory
     constexpr int VE = 16 / sizeof(T);
@@ -651,7 +749,12 @@ cudaError_t configure_unr(int bytes) {
 
 template <typename T>
 cudaError_t configure_typed(int bytes) {
-  return configure_unr<T, 4>(bytes);
+  constexpr int team = 3 * 8 * kTeamMaxThreads * (int)sizeof(float);
+  cudaError_t e = configure_unr<T, 4>(bytes), r;
+  if ((r = cudaFuncSetAttribute(row_fwd_team_kernel<T>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, team)) != cudaSuccess)
+    e = r;
+  return e;
 }
 
 }  // namespace
@@ -687,6 +790,7 @@ cudaError_t row_fwd_launch(int kind, int dtype, const RowFwdPtrs& p, int64_t R, 
   if (p.rng != nullptr) {
     a.rng = *p.rng;
     a.scale = p.rng->scale;
+    a.team = !vec_ok && p.rows_aligned && H <= kTeamMaxH ? team_threads(H) : 0;
     kind = kRowLnRng;
   }
   return dtype == GBN_F32 ? launch_typed<float>(kind, a, vec_ok, dev, st)

@@ -213,6 +213,9 @@ struct RowPlan {
   int cps = 1;         // blocks per SM the launch is sized for (fast path)
   int nstage = 0;      // pipeline depth (fast path)
   int G = 0;           // blocks (= rows of column partials)
+  int sms = 0;         // the device's, and its shared memory per block
+  int smem_optin = 0;
+  bool aligned = false;  // every tensor is 16-byte aligned
   int nout = 1;        // column outputs
   int nplanes = 1;     // 2 when fp32 outputs use hi/lo partials
   size_t smem = 0;     // dynamic shared memory per block
@@ -277,6 +280,7 @@ struct RowFwdPtrs {
   float* mean = nullptr;
   float* rstd = nullptr;
   const RngArgs* rng = nullptr;  // fused LayerNorm: the mask is drawn (mask null)
+  bool rows_aligned = false;     // drawn: x, residual, y and z are 16-byte aligned
 };
 
 // kind: GBN_ROW_RMS, GBN_ROW_LN or GBN_ROW_LN_FUSED.  vec_ok: every tensor

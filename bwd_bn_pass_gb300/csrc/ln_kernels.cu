@@ -42,6 +42,7 @@
 #include "gbn_internal.h"
 #include "philox.cuh"
 #include "row_engine.cuh"
+#include "row_team.cuh"
 
 namespace gbn {
 
@@ -67,6 +68,8 @@ struct LnArgs {
   int32_t Hv;
   int32_t nstage;
   int32_t nplanes;
+  int32_t team;      // a row team's threads (0: no teams)
+  int32_t team_par;  // its gamma and bias lie in shared memory
   int32_t zin;       // fused outputs from a saved z (x is z; no residual / bias)
   int32_t dres_f32;  // dresidual written as fp32
   uint32_t stage_bytes;
@@ -669,6 +672,207 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
   if (tid == 0 && sh.abort) ring_drain(sh, NS);
 }
 
+// The drawn mask for rows that the ring does not take, up to kTeamMaxH elements of
+// aligned tensors: a team of threads per row (row_team.cuh), a chunk of the row a
+// thread, z and dy in registers between the two passes.  Every team keeps its
+// column sums in shared memory, next to gamma and bias (fp32: those only where
+// they fit beside the six sums); a column changes hands from row to row, with a
+// barrier of the row's reduction in between.  At the end the teams' sums meet in
+// a fixed order and leave the block as its partial row.  The arithmetic is the
+// plain kernel's below.
+template <typename T>
+struct TeamCols {  // a team's per-column arrays, n words each
+  static constexpr bool COMP = sizeof(T) == 4;
+  static constexpr int kBytes = COMP ? 24 : 16;  // besides par's 8
+  float4* a;    // bf16: the three sums; fp32: sums 0 and 1 (hi, lo)
+  float2* b;    // fp32: sum 2
+  float2* par;  // gamma, bias; null where they stay in global memory
+  __device__ __forceinline__ TeamCols(unsigned char* base, int n, bool with_par)
+      : a(reinterpret_cast<float4*>(base)), b(reinterpret_cast<float2*>(base + 16 * n)),
+        par(with_par ? reinterpret_cast<float2*>(base + kBytes * n) : nullptr) {}
+};
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1) ln_bwd_team_kernel(const LnArgs a) {
+  using Cols = TeamCols<T>;
+  constexpr bool COMP = Cols::COMP;
+  extern __shared__ __align__(16) unsigned char tsm[];
+  __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  __shared__ float2 red[2][kTeamMaxThreads / 32];
+  const int H = a.H, P = team_pitch(H), n = 8 * P, TY = blockDim.x / a.team;
+  const int tbytes = n * (Cols::kBytes + (a.team_par ? 8 : 0));
+  RowTeam team(red, a.team);
+  const T* gamma = static_cast<const T*>(a.gamma);
+  const T* bias = static_cast<const T*>(a.bias);
+  // the next row's chunk is loaded while this one is worked on
+  int64_t r = (int64_t)blockIdx.x * TY + team.team;
+  const int64_t step = (int64_t)gridDim.x * TY;
+  RowChunk next(r, a.R, H, team.tx);
+  Raw8<T> xr, rr, dr;
+  float mu = 0.f, rho = 0.f;
+  auto load = [&] {
+    if (r < a.R && next.any()) {
+      xr.load(static_cast<const T*>(a.x) + next.at, next);
+      if (!a.zin) rr.load(static_cast<const T*>(a.res) + next.at, next);
+      dr.load(static_cast<const T*>(a.dy) + next.at, next);
+    }
+    if (r < a.R) {
+      mu = a.mean[r];
+      rho = a.rstd[r];
+    }
+  };
+  load();
+  philox_fill(keys, a.rng);
+  const Cols cols(tsm + team.team * tbytes, n, a.team_par);
+  for (int j = team.tx; j < H; j += team.TX) {
+    const int w = column_word(j, P);
+    cols.a[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (COMP) cols.b[w] = make_float2(0.f, 0.f);
+    if (cols.par) cols.par[w] = make_float2(to_f32(gamma[j]), bias ? to_f32(bias[j]) : 0.f);
+  }
+  __syncthreads();
+  Philox<true> gen;
+  gen.load(a.rng, keys);
+  const float fH = (float)H;
+  while (r < a.R) {
+    const RowChunk c = next;
+    const float m = mu, rs = rho;
+    float zh[8], zl[8], d[8];
+    uint32_t kept = 0;
+    float2 s = make_float2(0.f, 0.f);
+    auto param = [&](int e) {  // gamma and bias of element e
+      if (!COMP || a.team_par) return cols.par[c.word(e, team.tx, P)];
+      const int j = 8 * team.tx - c.s + e;
+      return make_float2(to_f32(gamma[j]), bias ? to_f32(bias[j]) : 0.f);
+    };
+    if (c.any()) {
+      kept = gen.bits((uint64_t)c.at >> 3);
+      dr.get(d);
+      xr.get(zh);
+      float rv[8];
+      if (!a.zin) rr.get(rv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool kp = (kept >> e) & 1u;
+        zl[e] = 0.f;
+        const float2 gb = c.has(e) ? param(e) : make_float2(0.f, 0.f);
+        if (!a.zin) {
+          const float xv = kp ? zh[e] : 0.f, bv = kp ? gb.y : 0.f;
+          if constexpr (COMP) {
+            const DF kt = df_mul(two_sum(xv, bv), kp ? a.scale : 0.f);
+            const DF z = df_plus(two_sum(rv[e], kt.hi), kt.lo);
+            zh[e] = z.hi;
+            zl[e] = z.lo;
+          } else {
+            zh[e] = fmaf(a.scale, xv + bv, rv[e]);
+          }
+        }
+        if (c.has(e)) {
+          const float gg = d[e] * gb.x;
+          s.x += gg;
+          s.y = fmaf(gg, (zh[e] - m) * rs, s.y);
+        }
+      }
+    }
+    r += step;
+    next = RowChunk(r, a.R, H, team.tx);
+    load();
+    s = team.sum(s);
+    if (!c.any()) continue;
+    const float mg = s.x / fH, mgx = s.y / fH;
+    float ex[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (a.dzx != nullptr) {
+      Raw8<float> er;
+      er.load(a.dzx + c.at, c);
+      er.get(ex);
+    }
+    float dz[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool kp = (kept >> e) & 1u, has = c.has(e);
+      const int w = c.word(e, team.tx, P);
+      const float gm = has ? param(e).x : 0.f;
+      if constexpr (COMP) {
+        const DF xh = df_mul(df_plus(two_sum(zh[e], -m), zl[e]), rs);
+        DF inner = df_plus(two_prod(d[e], gm), -mg);
+        const DF xm = df_mul(xh, mgx);
+        inner = df_plus(DF{inner.hi, inner.lo - xm.lo}, -xm.hi);
+        const DF z = df_plus(df_mul(inner, rs), ex[e]);
+        const DF dx = kp ? df_mul(z, a.scale) : DF{0.f, 0.f};
+        dz[e] = df_round(z);
+        zh[e] = df_round(dx);
+        if (has) {
+          const float4 p = cols.a[w];
+          DF s0{p.x, p.y}, s1{p.z, p.w};
+          df_acc(s0, df_mul(xh, d[e]));
+          df_add(s1, d[e]);
+          cols.a[w] = make_float4(s0.hi, s0.lo, s1.hi, s1.lo);
+          const float2 q = cols.b[w];
+          DF s2{q.x, q.y};
+          df_acc(s2, dx);
+          cols.b[w] = make_float2(s2.hi, s2.lo);
+        }
+      } else {
+        const float xh = (zh[e] - m) * rs;
+        dz[e] = fmaf(rs, d[e] * gm - mg - xh * mgx, ex[e]);
+        zh[e] = kp ? dz[e] * a.scale : 0.f;
+        if (has) {
+          const float4 p = cols.a[w];
+          cols.a[w] = make_float4(fmaf(d[e], xh, p.x), p.y + d[e], p.z + zh[e], 0.f);
+        }
+      }
+    }
+    chunk_store(static_cast<T*>(a.dx) + c.at, zh, c);
+    if (a.dres != nullptr) {
+      if (a.dres_f32) chunk_store(static_cast<float*>(a.dres) + c.at, dz, c);
+      else chunk_store(static_cast<T*>(a.dres) + c.at, dz, c);
+    }
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  // [output][plane][block][H]
+  const int64_t G = gridDim.x;
+  for (int j = threadIdx.x; j < H; j += blockDim.x) {
+    DF t[3] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    const int w = column_word(j, P);
+    for (int y = 0; y < TY; ++y) {
+      const Cols q(tsm + y * tbytes, n, a.team_par);
+      const float4 p = q.a[w];
+      if constexpr (COMP) {
+        const float2 p2 = q.b[w];
+        t[0] = df_sum(t[0], DF{p.x, p.y});
+        t[1] = df_sum(t[1], DF{p.z, p.w});
+        t[2] = df_sum(t[2], DF{p2.x, p2.y});
+      } else {
+        df_add(t[0], p.x);
+        df_add(t[1], p.y);
+        df_add(t[2], p.z);
+      }
+    }
+#pragma unroll
+    for (int o = 0; o < 3; ++o) {
+      float* out = a.part + (o * (COMP ? 2 : 1) * G + blockIdx.x) * H + j;
+      if constexpr (COMP) {
+        out[0] = t[o].hi;
+        out[G * H] = t[o].lo;
+      } else {
+        out[0] = df_round(t[o]);
+      }
+    }
+  }
+}
+
+// Threads of a block, at most: fp32's double-fp32 chain wants 128 registers.
+inline int team_block(bool f32, int team) { return f32 && team <= 512 ? 512 : 1024; }
+
+template <typename T>
+cudaError_t launch_team(const LnArgs& a, const RowPlan& p, cudaStream_t st) {
+  if constexpr (sizeof(T) == 4)
+    if (a.team <= 512)
+      return launch(ln_bwd_team_kernel<T, 512>, dim3(p.G), dim3(p.threads), p.smem, st, false, a);
+  return launch(ln_bwd_team_kernel<T, 1024>, dim3(p.G), dim3(p.threads), p.smem, st, false, a);
+}
+
 // Any H and alignment.  Block g owns rows g, g+G, ...; thread t owns columns
 // t, t+256, ...; column sums go straight into this block's partial rows.
 template <typename T, bool FUSED, int MASK>
@@ -812,6 +1016,8 @@ cudaError_t launch_ring(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
 // (at most 8), the counts the plan uses.
 template <typename T, bool FUSED, int MASK = kMaskBytes>
 cudaError_t launch_typed(const RowPlan& p, const LnArgs& a, cudaStream_t st) {
+  if constexpr (MASK == kMaskRng)
+    if (a.team != 0) return launch_team<T>(a, p, st);
   if (!p.fast)
     return launch(ln_bwd_generic_kernel<T, FUSED, MASK>, dim3(p.G), dim3(p.threads),
                   MASK == kMaskRng ? rowbits_bytes(a.H) : 0, st, false, a);
@@ -834,6 +1040,13 @@ cudaError_t set_smem(int bytes) {
 template <typename T>
 cudaError_t set_smem_all(int bytes) {
   cudaError_t e = cudaSuccess, r;
+  if constexpr (sizeof(T) == 4)
+    if ((r = cudaFuncSetAttribute(ln_bwd_team_kernel<T, 512>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+      e = r;
+  if ((r = cudaFuncSetAttribute(ln_bwd_team_kernel<T, 1024>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+    e = r;
   if ((r = set_smem<T, 1>(bytes)) != cudaSuccess) e = r;
   if constexpr (sizeof(T) == 2)
     if ((r = set_smem<T, 2>(bytes)) != cudaSuccess) e = r;
@@ -849,8 +1062,25 @@ cudaError_t ln_configure(int smem_optin) {
   return e1 != cudaSuccess ? e1 : e2;
 }
 
-cudaError_t ln_launch(const RowPlan& p, const LnPtrs& q, void* ws, int* status,
+cudaError_t ln_launch(const RowPlan& plan, const LnPtrs& q, void* ws, int* status,
                       cudaStream_t st) {
+  RowPlan p = plan;
+  int team = 0, team_par = 0;
+  if (q.rng != nullptr && !p.fast && p.aligned && p.H <= kTeamMaxH && p.R > 0) {
+    // row teams: one block per SM (no more of them than the plain kernel's, whose
+    // workspace they use)
+    team = team_threads(p.H);
+    const bool f32 = p.dtype == GBN_F32;
+    int64_t ty = teams_of_block(team, team_block(f32, team));
+    const int64_t want = (p.R + p.sms - 1) / p.sms;  // teams that find a row, every SM in use
+    if (ty > want) ty = want;
+    const int64_t cols = ty * 8 * team_pitch((int)p.H);
+    team_par = !f32 || cols * 32 <= p.smem_optin - kRowStaticSmem;
+    p.smem = (size_t)(cols * (f32 && team_par ? 32 : 24));
+    p.threads = (int)ty * team;
+    const int64_t blocks = (p.R + ty - 1) / ty;
+    p.G = (int)(blocks < p.sms ? blocks : p.sms);
+  }
   const bool fused = p.kind == GBN_ROW_LN_FUSED;
   void* outs[3] = {q.dgamma, q.dbeta, fused ? q.dbias : nullptr};
   if (p.R == 0 || p.H == 0)  // no rows: the column outputs are sums of nothing
@@ -880,6 +1110,8 @@ cudaError_t ln_launch(const RowPlan& p, const LnPtrs& q, void* ws, int* status,
   a.Hv = (int32_t)(p.H * (p.dtype == GBN_F32 ? 4 : 2) / 16);
   a.nstage = p.nstage;
   a.nplanes = p.nplanes;
+  a.team = team;
+  a.team_par = team_par;
   a.zin = q.saved_z ? 1 : 0;
   a.dres_f32 = q.dres_f32 ? 1 : 0;
   a.stage_bytes = p.stage_bytes;

@@ -96,6 +96,9 @@ bool row_plan(int64_t R, int64_t H, int kind, int dtype, bool fast_ok, bool has_
   p->R = R;
   p->H = H;
   p->kind = kind;
+  p->sms = dev.sms;
+  p->smem_optin = dev.smem_optin;
+  p->aligned = fast_ok;
   p->dtype = dtype;
   p->nout = kind == GBN_ROW_RMS ? 1 : (kind == GBN_ROW_LN ? 2 : 3);
   p->nplanes = dtype == GBN_F32 ? 2 : 1;

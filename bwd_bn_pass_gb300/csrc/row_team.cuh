@@ -1,0 +1,149 @@
+// Rows of any length for kernels with the drawn mask: a team of TX threads (whole
+// warps) takes a row, and thread tx its chunk tx -- eight adjacent elements that
+// start at a multiple of eight elements of the tensor, whatever the row's own
+// offset.  Chunks are therefore aligned for 16-byte loads and stores and are
+// exactly the generator's blocks; the first and the last of a row are shared with
+// its neighbours and masked.  Column j of a per-column array in shared memory lies
+// at (j mod 8)*P + j/8, so that the lanes of a warp (chunks in a row) meet
+// consecutive words whatever the offset.
+//
+// (One element a thread and column, the first form, needed five times the
+// instructions: LayerNorm backward bf16 [1636, 5498] 74 us.)
+#pragma once
+#include "gbn_common.cuh"
+#include "packed.cuh"
+#include "philox.cuh"
+
+namespace gbn {
+
+constexpr int kTeamMaxThreads = 1024;
+// every offset's chunks have to fit one block
+constexpr int64_t kTeamMaxH = 8 * kTeamMaxThreads - 7;
+
+// Threads of a row's team: whole warps over the chunks of the worst offset.
+inline int team_threads(int64_t H) { return (int)((H + 14) / 8 + 31) / 32 * 32; }
+// Words between the residues of a per-column array.
+__host__ __device__ inline int team_pitch(int H) { return (H + 7) / 8; }
+
+// Teams of a block of at most `threads`: named barriers 1 to 15 are theirs.
+inline int teams_of_block(int team, int threads) {
+  const int ty = threads / team;
+  return team > 32 && ty > 15 ? 15 : ty;
+}
+
+struct RowTeam {
+  float2 (*red)[kTeamMaxThreads / 32];  // [2]: warp sums, two rounds deep
+  int TX, team, tx, round = 0;
+  __device__ __forceinline__ RowTeam(float2 (*r)[kTeamMaxThreads / 32], int TX_)
+      : red(r), TX(TX_), team(threadIdx.x / TX_), tx(threadIdx.x % TX_) {}
+
+  __device__ __forceinline__ void sync() const {
+    if (TX == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(TX) : "memory");
+  }
+  // Sums over the team, in a fixed order.  One barrier: the buffer of the round
+  // before is not touched, and whoever is past this barrier has read it.
+  __device__ __forceinline__ float2 sum(float2 v) {
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (TX == 32) {
+      __syncwarp();
+      return v;
+    }
+    float2* buf = red[round & 1];
+    ++round;
+    const int lane = threadIdx.x & 31, nw = TX >> 5;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
+    sync();
+    const float2 t = lane < nw ? buf[team * nw + lane] : make_float2(0.f, 0.f);
+    return make_float2(warp_sum(t.x), warp_sum(t.y));
+  }
+};
+
+// A thread's chunk of row r.
+struct RowChunk {
+  int64_t at;    // its first element in the tensor
+  int s;         // the row's offset from its first chunk
+  int lo, hi;    // elements lo .. hi - 1 belong to the row (none: hi <= lo)
+  bool inside;   // all eight are within the tensor
+  __device__ __forceinline__ RowChunk(int64_t r, int64_t R, int H, int tx) {
+    const int64_t o = r * H;
+    s = (int)(o & 7);
+    at = (o - s) + 8 * tx;
+    lo = tx == 0 ? s : 0;
+    hi = min(8, H + s - 8 * tx);
+    inside = at + 8 <= R * H;
+  }
+  __device__ __forceinline__ bool any() const { return hi > lo; }
+  __device__ __forceinline__ bool full() const { return lo == 0 && hi == 8; }
+  __device__ __forceinline__ bool has(int e) const { return e >= lo && e < hi; }
+  // Word of element e's column in a per-column array (valid where has(e)).
+  __device__ __forceinline__ int word(int e, int tx, int P) const {
+    const int m = e - s;
+    return (m & 7) * P + tx + (m >> 3);
+  }
+};
+__device__ __forceinline__ int column_word(int j, int P) { return (j & 7) * P + (j >> 3); }
+
+// Eight elements, the ones past the tensor's end 0.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const bf16* p, const RowChunk& c) {
+    if (c.inside) {
+      v = *reinterpret_cast<const uint4*>(p);
+      return;
+    }
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    for (int e = 0; e < c.hi; ++e)
+      reinterpret_cast<uint16_t*>(w)[e] = reinterpret_cast<const uint16_t*>(p)[e];
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, const RowChunk& c) {
+    if (c.inside) {
+      a = *reinterpret_cast<const float4*>(p);
+      b = *reinterpret_cast<const float4*>(p + 4);
+      return;
+    }
+    float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int e = 0; e < c.hi; ++e) w[e] = p[e];
+    a = make_float4(w[0], w[1], w[2], w[3]);
+    b = make_float4(w[4], w[5], w[6], w[7]);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+// The row's elements of a chunk.
+template <typename T>
+__device__ __forceinline__ void chunk_store(T* p, const float (&f)[8], const RowChunk& c) {
+  if (c.full()) {
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      Vec<T, 8>::store(p, f);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c.has(e)) p[e] = from_f32<T>(f[e]);
+  }
+}
+
+}  // namespace gbn

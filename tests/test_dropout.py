@@ -320,6 +320,56 @@ def test_layernorm(gbn, dev, R, H, dtype):
     for k in ("dx", "dresidual", "dgamma", "dbeta", "dbias"):
         tol.check(bw[k], ref[k], f"ln bwd {R}x{H} {dtype} {k}", dtype)
 
+# rows that are no whole vectors: every offset from a chunk of eight, a chunk that
+# the tensor ends in, teams of one warp to a whole block, the longest team's row
+# and the first past it, fp32 rows whose gamma stays in global memory
+LN_TEAM_SHAPES = [(700, 9), (301, 37), (1300, 333), (613, 250), (50, 4081), (40, 4090), (5, 6999),
+                  (3, 7003), (3, 8185), (2, 8186), (2, 8191), (1, 15), (17, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,H", LN_TEAM_SHAPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layernorm_ragged(gbn, dev, R, H, dtype):
+    test_layernorm(gbn, dev, R, H, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,H,mis", [(61, 333, False), (5, 333, True), (3, 4097, False)])
+def test_layernorm_variants_ragged(gbn, dev, R, H, mis):
+    test_layernorm_variants(gbn, dev, R, H, mis)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layernorm_ragged_keeps_to_its_rows(gbn, dev, dtype):
+    """Rows next to the outputs, and infinities next to the inputs, that share
+    a row's first and last chunk: nothing of them is written or read."""
+    R, H, n = 5, 101, 8
+    dt = DT[dtype]
+    buf = torch.full((R * H + 2 * n,), float("inf"), device=dev, dtype=dt)
+    x = buf[n:n + R * H].view(R, H)
+    x.copy_(_rand((R, H), dtype, 91))
+    dy = buf.clone()[n:n + R * H].view(R, H)
+    r, g = _rand((R, H), dtype, 92), _rand((H,), dtype, 93)
+    outs = [torch.full_like(buf, 3.0) for _ in range(4)]
+    v = [t[n:n + R * H].view(R, H) for t in outs]
+    f = gbn.layernorm_dropout_forward(x, r, 0.2, (1, 2), g, y=v[0], z=v[1])
+    b = gbn.layernorm_dropout_backward(dy, x, r, f["mean"], f["rstd"], g, 0.2, (1, 2), dx=v[2],
+                                       dresidual=v[3])
+    for t in outs:
+        assert (t[:n] == 3).all() and (t[n + R * H:] == 3).all()
+        assert torch.isfinite(t).all()
+    whole = gbn.layernorm_dropout_forward(x.clone(), r, 0.2, (1, 2), g)
+    assert torch.equal(whole["y"], f["y"]) and torch.equal(whole["z"], f["z"])
+    assert all(torch.isfinite(b[k]).all() for k in b)
+    # a row that is not finite stays alone, in both of its neighbours' chunks
+    x[2] = float("nan")
+    f2 = gbn.layernorm_dropout_forward(x, r, 0.0, (1, 2), g)
+    f1 = gbn.layernorm_dropout_forward(torch.where(x.isnan(), 0.0, x), r, 0.0, (1, 2), g)
+    keep = [0, 1, 3, 4]
+    assert f2["y"][2].isnan().all() and torch.equal(f1["y"][keep], f2["y"][keep])
+
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("R,H,mis", [(40, 512, False), (9, 77, False), (6, 64, True),
