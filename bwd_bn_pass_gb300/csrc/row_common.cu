@@ -176,7 +176,15 @@ bool row_plan(int64_t R, int64_t H, int kind, int dtype, bool fast_ok, bool has_
       }
       const int64_t dyn = (int64_t)dev.smem_optin - kRowRingStatic;
       int64_t nst = dyn / (int64_t)off;
-      if (nst > kMaxStages) nst = kMaxStages;
+      if (nst > (rs > kMaxStages ? rs : kMaxStages)) nst = rs > kMaxStages ? rs : kMaxStages;
+      // Every slot belongs to one group (a whole number of slots each): a wait
+      // tells a slot's laps apart by one parity bit, so the lap before the awaited
+      // one has to be the same group's, which it has consumed.  With 14 groups on 8
+      // slots, groups 8 to 13 took their first wait (lap 1) for satisfied before lap
+      // 0 had landed: wrong sums, or a wait that ran out, once a block had more
+      // than eight stages of such narrow rows.
+      if (rs > nst) rs = nst;
+      if (rs > 0) nst -= nst % rs;
       // the slots' column sums are added in the idle ring at the end
       const uint64_t combine = (uint64_t)p->nout * p->nplanes * (uint64_t)H * 4;
       if (nst < 2 || combine > (uint64_t)dyn) {

@@ -22,7 +22,7 @@ namespace gbn {
 #define GBN_RING_TRACE(point) ((void)0)
 #endif
 
-constexpr int kRowMaxStages = 8;
+constexpr int kRowMaxStages = 14;
 constexpr int kRowStaticSmem = 4096;  // bound on a ring kernel's static shared memory
 
 // Static shared state of a ring kernel.
