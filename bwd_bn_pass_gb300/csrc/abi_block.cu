@@ -1,8 +1,8 @@
 // extern "C" entry points of the backbone-block operators (declared in
 // include/gbnorm.h): GroupNorm with an activation (channels last), RMSNorm of
 // attention heads with rotary positions, and dropout with a counter-based
-// mask, alone and inside LayerNorm.  As in abi.cu, arguments are validated before CUDA is touched,
-// and every call only launches on the caller's stream.
+// mask, alone and inside LayerNorm.  As in abi.cu, arguments are validated before
+// CUDA is touched, and every call only launches on the caller's stream.
 #include <cmath>
 
 #include "gbn_internal.h"
@@ -231,7 +231,7 @@ int gbn_gn_nhwc_backward(const void* x, const void* dy, int dtype, int64_t N, in
   const void* ptrs[3] = {x, dy, dx};
   GnPlan p;
   // at most four channels a thread: the sums' registers then leave four blocks
-  // per SM (eight: two), which the latency of two loads and an exponential needs
+  // per SM (eight channels: two), which the latency of two loads and an exponential needs
   const int width = bn_vec_width(dtype, C, ptrs, 3);
   if (!gn_plan(N, S, C, G, width < 4 ? width : 4, dtype == GBN_F32 ? 4 : 2, true, *dev, &p))
     return GBN_EINVAL;

@@ -35,8 +35,10 @@
 //
 // The fused form also runs with the counter-based mask of philox.cuh
 // (kRowLnRng), a dropped element contributing exactly 0 whatever it holds:
-// row_fwd_rng_kernel for rows of at most 256 vectors, else the kernels above
-// with the mask bytes replaced by the generator's bits.
+// row_fwd_rng_kernel for rows of at most 256 vectors (bf16 [8192, 1600] 27.8 us
+// with flushed caches, 3.8 TB/s; repeated 22.6), row_fwd_team_kernel for rows that
+// are no whole vectors (bf16 [8192, 1601] 56 us, [777, 1001] 11.4), else the
+// kernels above with the mask bytes replaced by the generator's bits.
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
 #include "packed.cuh"
