@@ -29,8 +29,11 @@
 // sum d^2 - (sum d)^2/4 loses at most a factor 4 to cancellation, whatever the
 // data), and merges the chunks pairwise (Chan, Golub, LeVeque, "Updating
 // formulae and a pairwise algorithm for computing sample variances", 1979): no
-// difference of large squares appears anywhere.  Means are kept relative to the
-// sample's first row (x[n, 0, c]), so a large common offset costs nothing.  All
+// difference of large squares appears anywhere.  Means of channels that lie far
+// from zero are kept relative to the sample's first row (gn_shift), so a large
+// offset costs nothing; the others are kept as they are, for a mean near zero
+// would be rounded at the size of that row's element (of its own size 3e-6 off in
+// fp32 groups of 1e4 elements, 1e-7 so).  All
 // combinations run in a fixed order: two runs give the same bits, and there are
 // no atomics.
 #include "gbn_common.cuh"
@@ -182,16 +185,25 @@ __device__ __forceinline__ f2 gn_gated(f2 d, f2 npre, float slope) {
 
 template <int VEC> constexpr int kGnStatsSmem = kGThreads * VEC * 12;
 
+// What a channel's means are kept relative to: its first element, where that is
+// far from zero next to the step to the second (the spread, about).  Unshifted, a
+// mean up to a few hundred spreads away leaves rounding errors of 1e-5 spreads,
+// whose squares alone reach the variance.
+__device__ __forceinline__ float gn_shift(float x0, float x1) {
+  return fabsf(x0) >= 256.f * fabsf(x1 - x0) ? x0 : 0.f;
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void gn_stats(const GnArgs& a, const GnBlock& b, unsigned char* smem) {
   constexpr int U = 4;  // rows of a chunk
   constexpr int NP = kPairs<VEC>;
   using V = Vec<T, VEC>;
   float2* acc = reinterpret_cast<float2*>(smem);  // [ty][channel of the tile]: mean - K, M2
-  float* Ks = reinterpret_cast<float*>(smem + kGThreads * VEC * 8);  // shifts: x[n, 0, c]
+  float* Ks = reinterpret_cast<float*>(smem + kGThreads * VEC * 8);  // shifts
   const GnGeom& g = a.g;
   const T* xs = static_cast<const T*>(a.x) + (int64_t)b.n * g.S * g.C;
   const int W = g.TX * VEC;  // channels of a full tile
+  const int second = g.S > 1 ? g.C : 0;  // from the first row to the second
   if (b.active) {
     const T* p = xs + (int64_t)b.cv * VEC;
     const T* xr = xs + (int64_t)b.r0 * g.C;
@@ -210,9 +222,17 @@ __device__ __forceinline__ void gn_stats(const GnArgs& a, const GnBlock& b, unsi
     int left = b.left;
     if (left > 0) load(q, left);
     f2 K[NP], mean[NP], M2[NP];
-    to_pairs<T, VEC>(V::ld(p), K);
+    {
+      f2 k1[NP];
+      to_pairs<T, VEC>(V::ld(p), K);
+      to_pairs<T, VEC>(V::ld(p + second), k1);
 #pragma unroll
-    for (int k = 0; k < NP; ++k) mean[k] = M2[k] = 0ull;
+      for (int k = 0; k < NP; ++k) {
+        const float2 u = f2_unpack(K[k]), v = f2_unpack(k1[k]);
+        K[k] = f2_pack(gn_shift(u.x, v.x), gn_shift(u.y, v.y));
+        mean[k] = M2[k] = 0ull;
+      }
+    }
     float cn = 0.f;
     while (left > 0) {
       f2 x0[NP], s[NP], sq[NP];
@@ -264,7 +284,8 @@ __device__ __forceinline__ void gn_stats(const GnArgs& a, const GnBlock& b, unsi
   const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto write = [&](int gi, float Kg, float mean, float q) {
     // relative to the shift of the group's first channel overall
-    const float K0 = gi * g.Cg >= b.c0 ? Kg : to_f32(xs[gi * g.Cg]);
+    const T* k = xs + gi * g.Cg;
+    const float K0 = gi * g.Cg >= b.c0 ? Kg : gn_shift(to_f32(k[0]), to_f32(k[second]));
     a.gpart[((int64_t)b.n * g.slices + b.slice) * g.E + gi + b.tile] =
         make_float2((Kg - K0) + mean, q);
     if (b.slice == 0 && gi * g.Cg >= b.c0) a.cpart[(int64_t)b.n * g.G + gi] = K0;
@@ -528,7 +549,9 @@ __device__ __forceinline__ void gn_apply(const GnArgs& a, const GnBlock& b, unsi
       [&](int gi, float(&acc)[2]) {
         const float cnt = (float)g.S * (float)g.Cg, dm = acc[0] / cnt;
         const float var = fmaxf(fmaf(-acc[0], dm, acc[1]), 0.f) / cnt;
-        const DF mu = two_sum(__ldcg(a.cpart + (int64_t)b.n * g.G + gi), m0 + dm);
+        const DF m = two_sum(m0, dm);
+        DF mu = two_sum(__ldcg(a.cpart + (int64_t)b.n * g.G + gi), m.hi);
+        mu = two_sum(mu.hi, mu.lo + m.lo);
         const float rstd = rsqrtf(var + a.eps);
         fin[gi - b.g0] = make_float3(mu.hi, mu.lo, rstd);
         if (b.slice == 0 && gi * g.Cg >= b.c0) {

@@ -308,3 +308,32 @@ def test_offsets_past_32_bits(gbn, dev):
     rows = one[0, -3:].double().view(3, 32, C // 32)
     pre = ((rows - m.view(1, 32, 1)) * r.view(1, 32, 1)).view(3, C)
     tol.check_bf16(y[N - 1, -3:], _f64(pre * torch.sigmoid(pre)), "last rows")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,S,C,G", [(1, 5000, 32, 32), (2, 20000, 6, 2), (3, 700, 640, 4),
+                                     (2, 64, 64, 1)])
+@pytest.mark.parametrize("offset", [0.0, 3.0, 1e4])
+def test_mean_keeps_its_bits(gbn, dev, dtype, N, S, C, G, offset):
+    """The saved mean (its two parts together) is off by at most the roundings of
+    the sums it is made of.  A thread merges at most ceil(rows / 4) <= 256 chunk
+    means, each merge rounding at the size of the running mean (below 4 spreads
+    beyond the shift, or 4 + offset where there is none) -- 2^-24 of it at worst,
+    but merged with weight 1 / merges, so that their sum stays below 12 (log2 of
+    the merges, and four more levels of the tree).  The shift is the offset itself
+    where that is 1e4 in fp32 (in bf16 the values there are 64 apart)."""
+    g = torch.Generator().manual_seed(N * S + C)
+    x = (torch.randn(N, S, C, generator=g) + offset).to(DT[dtype])
+    _, stats = gbn.gn_nhwc_forward_train(x.to(dev), G)
+    mean = x.double().view(N, S, G, -1).mean(dim=(1, 3))
+    got = stats[0].cpu().double() + stats[2].cpu().double()
+    size = 4.0 if offset > 100 and dtype == "f32" else 4.0 + offset
+    # errors of the threads are independent: their mean over T of them is 1 /
+    # sqrt(T) of one (four standard deviations of 12 * 2^-24 * size allowed)
+    threads = min(256, S) / 4
+    bound = 4 * 12 * 2.0 ** -24 * size / threads ** 0.5 + 2.0 ** -24 * mean.abs() * 2 ** -10
+    assert ((got - mean).abs() <= bound).all(), ((got - mean).abs() / bound).max()
+    if offset == 0.0:
+        # and never worse than 1e-6 of the means' size
+        assert (got - mean).norm() <= 1e-6 * mean.norm()
