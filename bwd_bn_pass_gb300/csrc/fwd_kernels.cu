@@ -604,9 +604,8 @@ template <typename T>
 cudaError_t launch_fwd_team(const FwdArgs& a, const DevInfo& dev, cudaStream_t st) {
   const size_t smem = (size_t)3 * 8 * team_pitch(a.H) * sizeof(float);
   // the longest rows alone need more than 512 threads; 64 registers a thread
-  int64_t ty = a.team <= 512 ? teams_of_block(a.team, 512) : 1;
-  const int64_t want = (a.R + 2 * dev.sms - 1) / (2 * dev.sms);
-  if (ty > want) ty = want;
+  const int64_t rows = (a.R + 2 * dev.sms - 1) / (2 * dev.sms);
+  const int64_t ty = teams_of_block(a.team, a.team <= 512 ? 512 : kTeamMaxThreads, rows);
   const int nt = (int)ty * a.team;
   const int64_t per_sm = 1024 / nt < 4 ? 1024 / nt : 4;
   const int64_t blocks = (a.R + ty - 1) / ty, cap = (int64_t)dev.sms * per_sm;

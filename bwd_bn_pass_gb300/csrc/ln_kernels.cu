@@ -1074,9 +1074,8 @@ cudaError_t ln_launch(const RowPlan& plan, const LnPtrs& q, void* ws, int* statu
     // workspace they use)
     team = team_threads(p.H);
     const bool f32 = p.dtype == GBN_F32;
-    int64_t ty = teams_of_block(team, team_block(f32, team));
-    const int64_t want = (p.R + p.sms - 1) / p.sms;  // teams that find a row, every SM in use
-    if (ty > want) ty = want;
+    // teams that find a row, every SM in use
+    const int64_t ty = teams_of_block(team, team_block(f32, team), (p.R + p.sms - 1) / p.sms);
     const int64_t cols = ty * 8 * team_pitch((int)p.H);
     team_par = !f32 || cols * 32 <= p.smem_optin - kRowStaticSmem;
     p.smem = (size_t)(cols * (f32 && team_par ? 32 : 24));

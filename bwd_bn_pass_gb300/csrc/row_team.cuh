@@ -1,5 +1,5 @@
-// Rows of any length for kernels with the drawn mask: a team of TX threads (whole
-// warps) takes a row, and thread tx its chunk tx -- eight adjacent elements that
+// Rows of any length for kernels with the drawn mask: a team of TX threads (8 or
+// 16 lanes of a warp, or whole warps) takes a row, and thread tx its chunk tx -- eight adjacent elements that
 // start at a multiple of eight elements of the tensor, whatever the row's own
 // offset.  Chunks are therefore aligned for 16-byte loads and stores and are
 // exactly the generator's blocks; the first and the last of a row are shared with
@@ -20,30 +20,48 @@ constexpr int kTeamMaxThreads = 1024;
 // every offset's chunks have to fit one block
 constexpr int64_t kTeamMaxH = 8 * kTeamMaxThreads - 7;
 
-// Threads of a row's team: whole warps over the chunks of the worst offset.
-inline int team_threads(int64_t H) { return (int)((H + 14) / 8 + 31) / 32 * 32; }
+// Threads of a row's team, over the chunks of the worst offset: 8, 16, or whole
+// warps.
+inline int team_threads(int64_t H) {
+  const int chunks = (int)((H + 14) / 8);
+  return chunks <= 8 ? 8 : chunks <= 16 ? 16 : (chunks + 31) / 32 * 32;
+}
 // Words between the residues of a per-column array.
 __host__ __device__ inline int team_pitch(int H) { return (H + 7) / 8; }
 
-// Teams of a block of at most `threads`: named barriers 1 to 15 are theirs.
-inline int teams_of_block(int team, int threads) {
-  const int ty = threads / team;
-  return team > 32 && ty > 15 ? 15 : ty;
+// Teams of a block of at most `threads`, no more than `rows`, but a whole warp at
+// least (which fills the generator's keys); named barriers 1 to 15 are theirs.
+inline int teams_of_block(int team, int threads, int64_t rows) {
+  int ty = threads / team;
+  if (team > 32 && ty > 15) ty = 15;
+  if (ty > rows) ty = (int)rows;
+  return ty * team < 32 ? 32 / team : ty;
 }
 
 struct RowTeam {
   float2 (*red)[kTeamMaxThreads / 32];  // [2]: warp sums, two rounds deep
   int TX, team, tx, round = 0;
+  uint32_t lanes;                  // the team's (or, of whole warps, all)
   __device__ __forceinline__ RowTeam(float2 (*r)[kTeamMaxThreads / 32], int TX_)
-      : red(r), TX(TX_), team(threadIdx.x / TX_), tx(threadIdx.x % TX_) {}
+      : red(r), TX(TX_), team(threadIdx.x / TX_), tx(threadIdx.x % TX_),
+        lanes(TX_ >= 32 ? 0xffffffffu : ((1u << TX_) - 1u) << (threadIdx.x & 31 & ~(TX_ - 1))) {}
 
   __device__ __forceinline__ void sync() const {
-    if (TX == 32) __syncwarp();
+    if (TX <= 32) __syncwarp(lanes);
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(TX) : "memory");
   }
   // Sums over the team, in a fixed order.  One barrier: the buffer of the round
   // before is not touched, and whoever is past this barrier has read it.
+  // (Teams of a part of a warp may be in different rows: only their lanes meet.)
   __device__ __forceinline__ float2 sum(float2 v) {
+    if (TX < 32) {
+      for (int o = TX / 2; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(lanes, v.x, o);
+        v.y += __shfl_xor_sync(lanes, v.y, o);
+      }
+      __syncwarp(lanes);
+      return v;
+    }
     v.x = warp_sum(v.x);
     v.y = warp_sum(v.y);
     if (TX == 32) {

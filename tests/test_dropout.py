@@ -324,7 +324,8 @@ def test_layernorm(gbn, dev, R, H, dtype):
 # the tensor ends in, teams of one warp to a whole block, the longest team's row
 # and the first past it, fp32 rows whose gamma stays in global memory
 LN_TEAM_SHAPES = [(700, 9), (301, 37), (1300, 333), (613, 250), (50, 4081), (40, 4090), (5, 6999),
-                  (3, 7003), (3, 8185), (2, 8186), (2, 8191), (1, 15), (17, 1)]
+                  (3, 7003), (3, 8185), (2, 8186), (2, 8191), (1, 15), (17, 1),
+                  (2001, 34), (999, 50), (1000, 51), (501, 113), (500, 114)]
 
 
 @pytest.mark.gpu
