@@ -9,11 +9,14 @@
 // of the copy rate; repeated 65 us, 6.2 TB/s); backward bf16 [8192, 1600] with the
 // bias gradient 21.6 us, in two launches.
 //
-// Two kernels:
+// Three kernels:
 //   * rows of whole 8-element chunks, 16-byte aligned tensors: a thread owns
 //     one chunk of columns (one generator block per row; the bias, or the
 //     bias gradient's sums, stay in registers) and strides down its block's
 //     slice of rows, several rows in flight;
+//   * other rows of aligned tensors, where no column is summed (forward, and the
+//     backward without the bias gradient): a thread owns a chunk of the flat
+//     tensor, whatever rows it spans, and walks the bias by the column;
 //   * everything else: a block owns 248 columns; eight rows at a time its 256
 //     threads draw the 8 x 32 blocks that cover them into shared memory as
 //     bits, then every thread walks its column.
@@ -195,6 +198,74 @@ __global__ void __launch_bounds__(kDThreads, kDBlocksPerSm)
   }
 }
 
+// Aligned tensors of any H, no column sums: the flat tensor in chunks of eight.
+// (Forward with bias and residual, bf16 [4096, 4097] 27.8 us, [65536, 3] 9.3; the
+// tile kernel below 68.7 and 44.1.)
+template <typename T>
+__global__ void __launch_bounds__(kDThreads, 4) dropout_flat_kernel(const DropArgs a) {
+  constexpr int U = 2;  // chunks in flight
+  using C8 = Chunk8<T>;
+  __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  philox_fill(keys, a.rng);
+  __syncthreads();
+  Philox<true> g;
+  g.load(a.rng, keys);
+  const f2 scale2 = f2_splat(a.rng.scale);
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.res);
+  const T* bias = static_cast<const T*>(a.bias);
+  T* y = static_cast<T*>(a.y);
+  const int64_t n = a.R * a.H, whole = n / 8, step = (int64_t)gridDim.x * kDThreads;
+  const int64_t c0 = (int64_t)blockIdx.x * kDThreads + threadIdx.x;
+  // the column of the chunk's first element, and its advance per chunk
+  int j = bias != nullptr ? (int)(8 * c0 % a.H) : 0;
+  const int jstep = bias != nullptr ? (int)(8 * step % a.H) : 0;
+  for (int64_t c = c0; c < whole; c += U * step) {
+    C8 cx[U], cr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c + u * step < whole) {
+        cx[u].load(x + 8 * (c + u * step));
+        if (res != nullptr) cr[u].load(res + 8 * (c + u * step));
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c + u * step >= whole) continue;
+      bool f[8];
+      f2 v[4], o[4] = {0ull, 0ull, 0ull, 0ull};
+      g.template keep<8>((uint64_t)(c + u * step) << 3, f);
+      cx[u].get(v);
+      if (res != nullptr) cr[u].get(o);
+      if (bias != nullptr) {
+        float b[8];
+        int jj = j;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          b[e] = to_f32(bias[jj]);
+          if (++jj == a.H) jj = 0;
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) v[p] = f2_add(v[p], f2_pack(b[2 * p], b[2 * p + 1]));
+        j += jstep;
+        if (j >= a.H) j -= a.H;
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float2 t = f2_unpack(v[p]);
+        o[p] = f2_fma(f2_pack(f[2 * p] ? t.x : 0.f, f[2 * p + 1] ? t.y : 0.f), scale2, o[p]);
+      }
+      C8::store(y + 8 * (c + u * step), o);
+    }
+  }
+  // the elements past the last whole chunk
+  const int64_t i = whole * 8 + threadIdx.x;
+  if (blockIdx.x == gridDim.x - 1 && i < n) {
+    const bool keep = (g.bits((uint64_t)whole) >> threadIdx.x) & 1u;
+    const float t = to_f32(x[i]) + (bias != nullptr ? to_f32(bias[i % a.H]) : 0.f);
+    y[i] = from_f32<T>(fmaf(keep ? t : 0.f, a.rng.scale, res != nullptr ? to_f32(res[i]) : 0.f));
+  }
+}
+
 // Any H and alignment.
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
@@ -263,6 +334,8 @@ cudaError_t launch_rows(const DropPlan& p, const DropArgs& a, bool bwd, cudaStre
 template <typename T>
 cudaError_t launch_drop(const DropPlan& p, const DropArgs& a, bool bwd, cudaStream_t st) {
   if (p.fast) return launch_rows<T>(p, a, bwd, st);
+  if (p.flat > 0 && a.part == nullptr)
+    return launch(dropout_flat_kernel<T>, dim3((unsigned)p.flat), dim3(kDThreads), 0, st, false, a);
   const dim3 grid((unsigned)p.gx, (unsigned)p.slices);
   return bwd ? launch(dropout_tile_kernel<T, true>, grid, dim3(kDThreads), 0, st, false, a)
              : launch(dropout_tile_kernel<T, false>, grid, dim3(kDThreads), 0, st, false, a);
@@ -285,6 +358,11 @@ RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state
 DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo& dev) {
   DropPlan p;
   p.fast = fast_ok && H % 8 == 0;
+  if (fast_ok && !p.fast) {
+    // two chunks a thread at least, every resident block slot once
+    const int64_t blocks = (R * H / 8 + 2 * kDThreads - 1) / (2 * kDThreads), cap = 4 * dev.sms;
+    p.flat = (int)(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+  }
   int64_t min_rows;
   if (p.fast) {
     // chunks of a block row: 32, 16 or 8 (at least 128 contiguous bytes),

@@ -381,10 +381,11 @@ constexpr int kDBlocksPerSm = 3;
 RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state);
 
 struct DropPlan {
-  bool fast = false;    // 8-element chunks per thread (else the tile kernel)
+  bool fast = false;    // 8-element chunks of a row per thread (else flat, or the tile kernel)
   int64_t gx = 1;       // column tiles
   int ltx = 0;          // fast: log2 of the chunks of a block's row
   int slices = 1;       // row slices (= rows of partial column sums)
+  int flat = 0;         // blocks of the flat kernel (0: tensors not aligned)
   size_t ws_bytes = 0;  // backward with dbias: the partials
 };
 // fast_ok: every tensor is 16-byte aligned.

@@ -1,0 +1,130 @@
+"""The native marshalling of the backbone-block calls: what it refuses, before
+anything is launched, and what it hands back."""
+
+import os
+
+import pytest
+import torch
+
+
+def test_missing_module_is_an_import_error(gbn, monkeypatch, tmp_path):
+    monkeypatch.setattr(gbn, "_block", None)
+    monkeypatch.setattr(gbn._build, "module_path", lambda: os.path.join(tmp_path, "_block.so"))
+    with pytest.raises(ImportError, match="build it with"):
+        gbn.dropout_forward(torch.zeros(2, 8), 0.1, (1, 2))
+
+
+def test_refusals_on_the_host(gbn):
+    x = torch.zeros(2, 3, 8)
+    for call in (lambda: gbn.gn_nhwc_forward_train(x, 2),
+                 lambda: gbn.gn_nhwc_backward(x, x, torch.zeros(3, 2, 2)),
+                 lambda: gbn.norm_rope_forward(x, torch.zeros(2), torch.zeros(4)),
+                 lambda: gbn.norm_rope_backward(x, x, torch.zeros(2), torch.zeros(4)),
+                 lambda: gbn.dropout_backward(x, 0.1, (1, 2)),
+                 lambda: gbn.layernorm_dropout_forward(x, x, 0.1, (1, 2)),
+                 lambda: gbn.layernorm_dropout_backward(x, x, x, x, x, x, 0.1, (1, 2)),
+                 lambda: gbn.dropout_forward(None, 0.1, (1, 2)),
+                 lambda: gbn.dropout_forward([1.0], 0.1, (1, 2))):
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):
+            call()
+    with pytest.raises(TypeError, match="arguments"):
+        gbn._native().dropout_forward(x)
+
+
+@pytest.fixture(scope="module")
+def t():
+    dev = "cuda:0"
+
+    class Tensors:
+        x = torch.zeros(4, 6, 16, device=dev)
+        flat = torch.zeros(4, 16, device=dev)
+        c = torch.ones(16, device=dev)
+        half = torch.ones(16, device=dev, dtype=torch.float16)
+        b16 = torch.ones(16, device=dev, dtype=torch.bfloat16)
+        short = torch.ones(15, device=dev)
+        rows = torch.zeros(4, device=dev)
+        stats = torch.ones(3, 4, 2, device=dev)
+        pos = torch.zeros(4, device=dev, dtype=torch.int64)
+        tab = torch.zeros(8, device=dev, dtype=torch.int64)
+        w = torch.ones(16, device=dev)
+        rstd = torch.ones(4, 6, device=dev)
+        cpu = torch.ones(16)
+    return Tensors
+
+
+CASES = [
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x, 3)),
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x, 0)),
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x, 2, act="gelu")),
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x, 2, t.short)),
+    (TypeError, lambda G, t: G.gn_nhwc_forward_train(t.x, 2, t.b16)),
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x, 2, t.cpu)),
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x, 2, y=t.flat)),
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x, 2, stats=t.rows)),
+    (TypeError, lambda G, t: G.gn_nhwc_forward_train(t.x, "2")),
+    (TypeError, lambda G, t: G.gn_nhwc_forward_train(t.x, 2, eps="1")),
+    (TypeError, lambda G, t: G.gn_nhwc_forward_train(t.x.half(), 2)),
+    (ValueError, lambda G, t: G.gn_nhwc_forward_train(t.x.transpose(0, 1), 2)),
+    (ValueError, lambda G, t: G.gn_nhwc_backward(t.x, t.x, t.rows)),
+    (ValueError, lambda G, t: G.gn_nhwc_backward(t.x, t.flat, t.stats)),
+    (ValueError, lambda G, t: G.gn_nhwc_backward(t.x, t.x, t.stats, dgamma=t.short)),
+    (ValueError, lambda G, t: G.norm_rope_forward(t.x, t.pos[:3], t.tab)),
+    (TypeError, lambda G, t: G.norm_rope_forward(t.x, t.rows, t.tab)),
+    (TypeError, lambda G, t: G.norm_rope_forward(t.x, t.pos, t.rows)),
+    (ValueError, lambda G, t: G.norm_rope_forward(t.x, t.pos, t.tab, t.w, q_heads=2)),
+    (ValueError, lambda G, t: G.norm_rope_forward(t.x, t.pos, t.tab, t.b16)),
+    (ValueError, lambda G, t: G.norm_rope_forward(t.x, t.pos, t.tab, layout="pairs")),
+    (ValueError, lambda G, t: G.norm_rope_forward(t.x, t.pos, t.tab, y=t.flat)),
+    (ValueError, lambda G, t: G.norm_rope_forward(t.flat, t.pos, t.tab)),
+    (ValueError, lambda G, t: G.norm_rope_backward(t.x, t.x, t.pos, t.tab, None, t.w)),
+    (ValueError, lambda G, t: G.norm_rope_backward(t.x, None, t.pos, t.tab, t.rstd, t.w)),
+    (ValueError, lambda G, t: G.norm_rope_backward(t.x, t.x, t.pos, t.tab, dwq=t.w)),
+    (ValueError, lambda G, t: G.dropout_forward(t.flat, 0.1, (1, 2), bias=t.short)),
+    (ValueError, lambda G, t: G.dropout_forward(t.flat, 0.1, (1, 2), residual=t.x)),
+    (TypeError, lambda G, t: G.dropout_forward(t.flat, 0.1, (1,))),
+    (TypeError, lambda G, t: G.dropout_forward(t.flat, 0.1, 5)),
+    (TypeError, lambda G, t: G.dropout_forward(t.flat, 0.1, ("a", 2))),
+    (TypeError, lambda G, t: G.dropout_forward(t.flat, None, (1, 2))),
+    (ValueError, lambda G, t: G.dropout_backward(t.flat, 0.1, (1, 2), dbias=t.b16)),
+    (ValueError, lambda G, t: G.layernorm_dropout_forward(t.flat, t.x, 0.1, (1, 2))),
+    (TypeError, lambda G, t: G.layernorm_dropout_forward(t.flat, t.flat, 0.1, (1, 2),
+                                                         mean=t.b16[:4])),
+    (ValueError, lambda G, t: G.layernorm_dropout_backward(t.flat, t.flat, None, t.rows, t.rows,
+                                                           t.c, 0.1, (1, 2))),
+    (ValueError, lambda G, t: G.layernorm_dropout_backward(t.flat, t.flat, t.flat, t.rows, t.rows,
+                                                           None, 0.1, (1, 2))),
+    (ValueError, lambda G, t: G.layernorm_dropout_backward(t.flat, t.flat, t.flat, t.rows, t.rows,
+                                                           t.c, 0.1, (1, 2), dx=t.x)),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", range(len(CASES)))
+def test_refusals(gbn, t, k):
+    error, call = CASES[k]
+    with pytest.raises(error):
+        call(gbn, t)
+
+
+@pytest.mark.gpu
+def test_status_becomes_the_libraries_error(gbn, t):
+    with pytest.raises(gbn.GbnError) as e:
+        gbn.dropout_forward(t.flat, 1.5, (1, 2))
+    assert e.value.status == -1 and "gbn_dropout_forward" in str(e.value)
+    with pytest.raises(gbn.GbnError):   # a workspace too small
+        gbn.gn_nhwc_backward(t.x, t.x, t.stats, ws=torch.empty(16, dtype=torch.uint8,
+                                                               device="cuda:0"))
+
+
+@pytest.mark.gpu
+def test_given_outputs_come_back(gbn, t):
+    y = torch.empty_like(t.flat)
+    assert gbn.dropout_forward(t.flat, 0.5, (1, 2), y=y) is y
+    dx, db = gbn.dropout_backward(t.flat, 0.5, [1, 2])
+    assert db is None and dx.shape == t.flat.shape
+    out, rstd = gbn.norm_rope_forward(t.x, t.pos, t.tab)
+    assert rstd is None and out.shape == t.x.shape
+    # seeds are taken modulo 2^64, numbers of any integer type
+    a = gbn.dropout_forward(torch.ones_like(t.flat), 0.5, (2 ** 64 + 3, -1))
+    b = gbn.dropout_forward(torch.ones_like(t.flat), 0.5, (3, 2 ** 64 - 1))
+    assert torch.equal(a, b)

@@ -192,6 +192,23 @@ def test_backward(gbn, dev, R, H, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,H", [(70001, 3), (5003, 21), (2, 131), (90000, 1), (9, 20001)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_flat_chunks(gbn, dev, R, H, dtype):
+    """Chunks that span rows: several a thread, the tail past the last whole one,
+    the bias by its column; in place; the bias gradient's kernel draws the same."""
+    test_forward(gbn, dev, R, H, dtype)
+    dy = _rand((R, H), dtype, 6)
+    a, _ = gbn.dropout_backward(dy, 0.25, (SEED, OFFSET))
+    b, _ = gbn.dropout_backward(dy, 0.25, (SEED, OFFSET), want_dbias=True)
+    assert torch.equal(a, b)
+    bias = _rand((H,), dtype, 7)
+    want = gbn.dropout_forward(dy, 0.25, (SEED, OFFSET), bias=bias, residual=dy)
+    assert torch.equal(gbn.dropout_forward(dy, 0.25, (SEED, OFFSET), bias=bias, residual=dy, y=dy),
+                       want)
+
+
+@pytest.mark.gpu
 def test_mask_does_not_depend_on_type_or_alignment(gbn, dev):
     ones = torch.ones(21, 136, device=dev)
     ref = oracle.dropout_mask(21 * 136, 0.3, 12, 34).reshape(21, 136)
