@@ -73,7 +73,7 @@ const DevInfo* device_info(int device) {
   if (row_kernels_configure(n.smem_optin) != cudaSuccess) return nullptr;
   if (bn_fused_configure(n.smem_optin, &n.fused_ok) != cudaSuccess) return nullptr;
   if (row_fwd_configure() != cudaSuccess) return nullptr;
-  if (rope_configure() != cudaSuccess) return nullptr;
+  if (rope_configure() != cudaSuccess || drop_configure() != cudaSuccess) return nullptr;
   n.ok = true;
   d = n;
   return &d;

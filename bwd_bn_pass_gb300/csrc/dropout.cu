@@ -9,7 +9,7 @@
 // of the copy rate; repeated 65 us, 6.2 TB/s); backward bf16 [8192, 1600] with the
 // bias gradient 21.6 us, in two launches.
 //
-// Three kernels:
+// Four kernels:
 //   * rows of whole 8-element chunks, 16-byte aligned tensors: a thread owns
 //     one chunk of columns (one generator block per row; the bias, or the
 //     bias gradient's sums, stay in registers) and strides down its block's
@@ -17,15 +17,21 @@
 //   * other rows of aligned tensors, where no column is summed (forward, and the
 //     backward without the bias gradient): a thread owns a chunk of the flat
 //     tensor, whatever rows it spans, and walks the bias by the column;
+//   * the backward with the bias gradient over such rows of at most kTeamMaxH
+//     elements: a team of threads per row (row_team.cuh), the column sums in
+//     shared memory;
 //   * everything else: a block owns 248 columns; eight rows at a time its 256
 //     threads draw the 8 x 32 blocks that cover them into shared memory as
 //     bits, then every thread walks its column.
 // The bias gradient's per-block partial rows are added in a fixed order by
 // colsum_kernel (no atomics).
+#include <type_traits>
+
 #include "gbn_common.cuh"
 #include "gbn_internal.h"
 #include "packed.cuh"
 #include "philox.cuh"
+#include "row_team.cuh"
 
 namespace gbn {
 
@@ -34,6 +40,7 @@ namespace {
 constexpr int kDThreads = 256;
 constexpr int kDTileCols = 248;  // 248 + 7 elements span at most 32 blocks
 constexpr int kDTileRows = 8;
+constexpr int kDTeamThreads = 1024;  // team kernel: at most
 
 struct DropArgs {
   const void* x;     // forward input / dy
@@ -46,6 +53,7 @@ struct DropArgs {
   int32_t Hc;        // chunks per row (rows kernel)
   int32_t ltx;       // rows kernel: log2 of the block's chunks per row
   int32_t slices;
+  int32_t team;      // team kernel: threads of a row
   RngArgs rng;
 };
 
@@ -266,6 +274,73 @@ __global__ void __launch_bounds__(kDThreads, 4) dropout_flat_kernel(const DropAr
   }
 }
 
+// Backward with the bias gradient, aligned tensors, H <= kTeamMaxH.  A column's sum
+// changes hands from row to row (a chunk starts at another column there), with the
+// team's barrier in between.  bf16 [4096, 4097] 44 us (the tile kernel 65), [20000,
+// 101] 15.5 (25.7), [65536, 3] 17.5 (42).
+template <typename T>
+__global__ void __launch_bounds__(kDTeamThreads, 1) dropout_team_kernel(const DropArgs a) {
+  constexpr bool COMP = sizeof(T) == 4;
+  using Sum = typename std::conditional<COMP, float2, float>::type;
+  extern __shared__ __align__(16) unsigned char tsm[];
+  __shared__ __align__(16) uint32_t keys[kPhiloxKeys];
+  const int H = a.H, P = team_pitch(H), n = 8 * P, TY = blockDim.x / a.team;
+  RowTeam team(nullptr, a.team);
+  Sum* sums = reinterpret_cast<Sum*>(tsm);
+  Sum* cols = sums + (size_t)team.team * n;
+  int64_t r = (int64_t)blockIdx.x * TY + team.team;
+  const int64_t step = (int64_t)gridDim.x * TY;
+  RowChunk next(r, a.R, H, team.tx);
+  Raw8<T> raw;
+  auto load = [&] {
+    if (r < a.R && next.any()) raw.load(static_cast<const T*>(a.x) + next.at, next);
+  };
+  load();
+  philox_fill(keys, a.rng);
+  for (int j = threadIdx.x; j < TY * n; j += blockDim.x) sums[j] = Sum{};
+  __syncthreads();
+  Philox<true> gen;
+  gen.load(a.rng, keys);
+  while (r < a.R) {
+    const RowChunk c = next;
+    float v[8];
+    if (c.any()) raw.get(v);
+    r += step;
+    next = RowChunk(r, a.R, H, team.tx);
+    load();
+    if (c.any()) {
+      const uint32_t kept = gen.bits((uint64_t)c.at >> 3);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = (kept >> e) & 1u ? v[e] * a.rng.scale : 0.f;
+        if (!c.has(e)) continue;
+        Sum& s = cols[c.word(e, team.tx, P)];
+        if constexpr (COMP) {
+          DF t{s.x, s.y};
+          df_add(t, v[e]);
+          s = make_float2(t.hi, t.lo);
+        } else {
+          s += v[e];
+        }
+      }
+      chunk_store(static_cast<T*>(a.y) + c.at, v, c);
+    }
+    team.sync();
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  for (int j = threadIdx.x; j < H; j += blockDim.x) {
+    ColSum<T> t;
+    for (int y = 0; y < TY; ++y) {
+      const Sum s = sums[(size_t)y * n + column_word(j, P)];
+      if constexpr (COMP) t.add(DF{s.x, s.y});
+      else t.add(s);
+    }
+    a.part[(int64_t)blockIdx.x * H + j] = t.s.hi;
+    if constexpr (COMP) a.part[((int64_t)gridDim.x + blockIdx.x) * H + j] = t.s.lo;
+  }
+}
+
 // Any H and alignment.
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kDThreads) dropout_tile_kernel(DropArgs a) {
@@ -336,6 +411,10 @@ cudaError_t launch_drop(const DropPlan& p, const DropArgs& a, bool bwd, cudaStre
   if (p.fast) return launch_rows<T>(p, a, bwd, st);
   if (p.flat > 0 && a.part == nullptr)
     return launch(dropout_flat_kernel<T>, dim3((unsigned)p.flat), dim3(kDThreads), 0, st, false, a);
+  if (p.team > 0)
+    return launch(dropout_team_kernel<T>, dim3((unsigned)p.team_blocks), dim3((unsigned)p.threads),
+                  (size_t)(p.threads / p.team) * 8 * team_pitch(a.H) * (sizeof(T) == 4 ? 8 : 4), st,
+                  false, a);
   const dim3 grid((unsigned)p.gx, (unsigned)p.slices);
   return bwd ? launch(dropout_tile_kernel<T, true>, grid, dim3(kDThreads), 0, st, false, a)
              : launch(dropout_tile_kernel<T, false>, grid, dim3(kDThreads), 0, st, false, a);
@@ -353,6 +432,11 @@ RngArgs make_rng(double p, uint64_t seed, uint64_t offset, const uint64_t* state
   r.lim = thr << 16;
   r.scale = thr ? (float)(65536.0 / (double)thr) : 0.f;
   return r;
+}
+
+cudaError_t drop_configure() {  // one long row's double-fp32 sums
+  return cudaFuncSetAttribute(dropout_team_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              8 * kTeamMaxThreads * (int)sizeof(float2));
 }
 
 DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo& dev) {
@@ -387,6 +471,18 @@ DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo&
   if (s < 1) s = 1;
   if (s > 65535) s = 65535;
   p.slices = (int)s;
+  if (fast_ok && !p.fast && H <= kTeamMaxH) {
+    // two blocks of up to 512 threads an SM (one of a longer row's), a row a team
+    // at least
+    p.team = team_threads(H);
+    const int most = p.team <= 512 ? 512 : kDTeamThreads;
+    const int64_t cap = p.team <= 512 ? 2 * dev.sms : dev.sms;
+    const int ty = teams_of_block(p.team, most, (R + cap - 1) / cap);
+    p.threads = ty * p.team;
+    const int64_t blocks = (R + ty - 1) / ty;
+    p.team_blocks = (int)(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+    if (s < p.team_blocks) s = p.team_blocks;
+  }
   p.ws_bytes = ((size_t)(dtype == GBN_F32 ? 2 : 1) * (size_t)s * (size_t)H * 4 + 255) & ~(size_t)255;
   return p;
 }
@@ -394,19 +490,20 @@ DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo&
 cudaError_t drop_forward(const DropPlan& p, int dtype, const void* x, const void* bias,
                          const void* res, void* y, int64_t R, int64_t H, const RngArgs& rng,
                          cudaStream_t st) {
-  DropArgs a{x, res, bias, y, nullptr, R, (int32_t)H, (int32_t)(H / 8), p.ltx, p.slices, rng};
+  DropArgs a{x, res, bias, y, nullptr, R, (int32_t)H, (int32_t)(H / 8), p.ltx, p.slices, 0, rng};
   return dtype == GBN_F32 ? launch_drop<float>(p, a, false, st) : launch_drop<bf16>(p, a, false, st);
 }
 
 cudaError_t drop_backward(const DropPlan& p, int dtype, const void* dy, void* dx, void* dbias,
                           void* ws, int64_t R, int64_t H, const RngArgs& rng, cudaStream_t st) {
   DropArgs a{dy, nullptr, nullptr, dx, dbias ? static_cast<float*>(ws) : nullptr, R, (int32_t)H,
-             (int32_t)(H / 8), p.ltx, p.slices, rng};
+             (int32_t)(H / 8), p.ltx, p.slices, p.team, rng};
   cudaError_t e =
       dtype == GBN_F32 ? launch_drop<float>(p, a, true, st) : launch_drop<bf16>(p, a, true, st);
   if (e != cudaSuccess || dbias == nullptr) return e;
   void* outs[3] = {dbias, nullptr, nullptr};
-  return colsum_launch(a.part, 1, dtype == GBN_F32 ? 2 : 1, p.slices, H, dtype, outs, st, true);
+  return colsum_launch(a.part, 1, dtype == GBN_F32 ? 2 : 1, p.team > 0 ? p.team_blocks : p.slices, H,
+                       dtype, outs, st, true);
 }
 
 }  // namespace gbn

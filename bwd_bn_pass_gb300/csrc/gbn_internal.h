@@ -386,8 +386,11 @@ struct DropPlan {
   int ltx = 0;          // fast: log2 of the chunks of a block's row
   int slices = 1;       // row slices (= rows of partial column sums)
   int flat = 0;         // blocks of the flat kernel (0: tensors not aligned)
+  int team = 0;         // team kernel: threads of a row's team (0: the tile kernel)
+  int threads = 0, team_blocks = 0;
   size_t ws_bytes = 0;  // backward with dbias: the partials
 };
+cudaError_t drop_configure();  // shared-memory limits (called from device_info)
 // fast_ok: every tensor is 16-byte aligned.
 DropPlan drop_plan(int64_t R, int64_t H, bool fast_ok, int dtype, const DevInfo& dev);
 cudaError_t drop_forward(const DropPlan& p, int dtype, const void* x, const void* bias,

@@ -192,12 +192,14 @@ def test_backward(gbn, dev, R, H, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("R,H", [(70001, 3), (5003, 21), (2, 131), (90000, 1), (9, 20001)])
+@pytest.mark.parametrize("R,H", [(70001, 3), (5003, 21), (2, 131), (90000, 1), (9, 20001),
+                                 (40, 4099), (7, 8185), (5, 8186), (6, 8191), (1300, 115)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_flat_chunks(gbn, dev, R, H, dtype):
     """Chunks that span rows: several a thread, the tail past the last whole one,
     the bias by its column; in place; the bias gradient's kernel draws the same."""
     test_forward(gbn, dev, R, H, dtype)
+    test_backward(gbn, dev, R, H, dtype)
     dy = _rand((R, H), dtype, 6)
     a, _ = gbn.dropout_backward(dy, 0.25, (SEED, OFFSET))
     b, _ = gbn.dropout_backward(dy, 0.25, (SEED, OFFSET), want_dbias=True)
