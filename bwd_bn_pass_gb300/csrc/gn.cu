@@ -11,8 +11,9 @@
 // Bound: DRAM traffic, x (and dy) read once and the output written once; the
 // second read of the inputs comes from L2 where they fit.  Measured, caches
 // flushed, SILU: forward bf16 [8, 64, 64, 320] 23.7 us (stats and apply, 21 MB
-// in); backward bf16 [64, 64, 64, 512] 240 us, where the inputs (537 MB) are read
-// from DRAM twice: sums 101 us (5.3 TB/s), dx 129 us (6.2 TB/s).
+// in); backward bf16 [64, 64, 64, 512] 231 us, where the inputs (537 MB) are read
+// from DRAM twice: sums 98 us (5.5 TB/s), dx with the weight gradients 123 us (6.5
+// TB/s).
 // Running the two passes over groups of samples that fit L2 was slower (302 to 440
 // us by the size of the group: every group's launches start and drain the SMs).
 // Small samples (kGnSmallRows) take one launch: forward fp32 [1, 8, 8, 64] 13.4 us.

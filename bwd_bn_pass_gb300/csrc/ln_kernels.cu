@@ -680,7 +680,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1) ln_bwd_ring_kernel(const L
 // barrier of the row's reduction in between.  At the end the teams' sums meet in
 // a fixed order and leave the block as its partial row.  The arithmetic is the
 // plain kernel's below, which keeps its sums in global memory: fp32 [777, 1001] 40
-// us there, 25.7 here; fp32 [1636, 5498] 367 and 138; bf16 [60, 8191] 89 there,
+// us there, 27.8 here; fp32 [1636, 5498] 367 and 138; bf16 [60, 8191] 89 there,
 // [60, 8185] 30 here.  Bound: issue (fp32: long double-fp32 chains).
 template <typename T>
 struct TeamCols {  // a team's per-column arrays, n words each
@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(NT, 1) ln_bwd_team_kernel(const LnArgs a) {
 }
 
 // Threads of a block, at most: fp32's double-fp32 chain wants 128 registers (fp32
-// [777, 1001] 25.7 us; 40 with 1024 threads of 64, which spill).
+// [777, 1001] 27.8 us; 40 with 1024 threads of 64, which spill).
 inline int team_block(bool f32, int team) { return f32 && team <= 512 ? 512 : 1024; }
 
 template <typename T>
